@@ -94,6 +94,8 @@ def _draw(rng, op):
         new = _log(rng, 2, 1024)
         batch, cached = _log(rng, 1, max(1, 2048 // new)), new + _log(rng, 1, 15360)
         blocks = min(blocks, 1024 // page)
+    if op == "select":      # more blocks than are picked: otherwise nothing is chosen
+        cached = new + _log(rng, 4 * blocks * page, 8 * blocks * page if new > 1 else 131072)
     return dict(op=op, batch=batch, new=new, cached=cached, blocks=max(blocks, 2), **heads)
 
 
@@ -272,10 +274,10 @@ def _quantise(mean):
     """Codes and a power of two for each vector: the smallest 2^e with max|mean| <= 2^(e + 7), at least 2^-126."""
     top = mean.abs().amax(-1)
     _, e = torch.frexp(top)
-    scale = torch.ldexp(torch.ones_like(top), (e - 7).clamp(min=-126))
+    scale = ((e - 7).clamp(min=-126, max=127) + 127).int().bitwise_left_shift(23).view(torch.float32)   # the power by its bits
     scale = torch.where(top > 0, scale, 1.0)
     codes = torch.round(mean / scale[..., None]).clamp(-127, 127)
-    return codes.to(torch.int8), scale.float()
+    return codes.to(torch.int8), scale
 
 
 def _write_plain(s):
