@@ -1,0 +1,386 @@
+// Attention of single rows (new tokens) over a paged cache, whole
+// (sgdn_paged_attend) or by a list of blocks (sgdn_paged_attend_sparse).
+//
+// For one row, key/value head and tile of up to 16 of the group's query heads
+// the keys are walked in tiles of 32.  With x = scale log2(e) K q and a running
+// reference c >= max x - const per query head:
+//   p = 2^(x - c),  l += sum p,  A += V^T p;   c' > c: l, A *= 2^(c - c')
+//   o = A / l,  lse = (c + log2 l) ln 2
+// Partial results (c, l, A) of waves and splits join by the same rule.
+//
+// Both products run transposed, so that nothing crosses lanes between them:
+//   S^T [32 keys x 16 heads] = K Q^T: the keys enter as the rows of A in the
+//     order  row 4m + j of tile a = key 8m + 4a + j,  so that lane (n, g)
+//     receives keys 8g .. 8g+7 of head n: the B operand of the next product;
+//   A^T [D x 16 heads] += V^T P^T: V^T needs eight keys per lane.  Lane (n, g)
+//     loads D/16 neighbouring elements of keys 8g .. 8g+7 (whole rows by the
+//     16 lanes of a g) and transposes its 8 x D/16 square with byte
+//     permutations; row i of product c then is element i D/16 + c.
+// K and V go from global memory to registers, without LDS: no two waves of a
+// workgroup read the same keys.  The next tile's K is requested when the
+// scores are done and the next V when the weights are applied, so that a wave
+// has 16 KiB (D = 128) on its way at all times.
+//
+// The reference c moves only where x exceeds it by 4 + BIAS, which after a few
+// tiles is rare.  fp16 weights are kept up to 2^(BIAS + 4) instead of 2^4: the
+// type holds 2^-14 with full accuracy, and BIAS = 10 puts that at 2^-24 of the
+// largest weight.
+//
+// Bound: HBM, each key and value once per row.  (At most 16 of 16 columns of
+// the products are used; at 16 heads a group that is 4 flops a byte.)
+#include "common.h"
+#include "paged.h"
+
+namespace sgdn {
+
+namespace {
+
+constexpr int NW = 4;        // waves of a workgroup
+constexpr int KT = 32;       // keys of a tile
+
+template <typename E> struct Bias { static constexpr float V = 0.f; };
+template <> struct Bias<fp16> { static constexpr float V = 10.f; };
+
+// V^T fragment of element c of every lane's D/16 (16-bit elements, two per word).
+template <typename E, int DW> __device__ __forceinline__ frag_t<E> v_frag(const uint32_t (&v)[8][DW], int c) {
+  if constexpr (sizeof(E) == 2) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+    u32x4 w;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] = __builtin_amdgcn_perm(v[2 * d + 1][c >> 1], v[2 * d][c >> 1], sel);
+    return __builtin_bit_cast(frag_t<E>, w);
+  } else {
+    frag_t<E> f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __builtin_bit_cast(float, v[j][c]);
+    return f;
+  }
+}
+
+template <typename E> __device__ __forceinline__ frag_t<E> ld8a(const E* p) {   // 16-byte aligned
+  if constexpr (sizeof(E) == 2) {
+    return ld8(p);
+  } else {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+    return cat44(a, b);
+  }
+}
+
+// Where 16 keys lie: their first row (of D elements) in the caches, and how
+// many of them take part.
+struct Half { size_t row; int n; };
+
+template <typename E, typename O, int D, bool SPARSE>
+__global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel(PageAttendArgs a, int units) {
+  constexpr int NS = D / 32;                     // reduction steps of the scores
+  constexpr int EPL = D / 16;                    // elements of V per lane and key
+  constexpr int DW = EPL * (int)sizeof(E) / 4;   // the same in words
+  constexpr bool TWO = sizeof(E) == 2 && sizeof(O) == 4;   // weights in two parts
+  constexpr float BIAS = Bias<E>::V;
+  constexpr int LD = D + 4;                      // LDS row: the pad spreads heads over banks
+  __shared__ float joined[NW][16][LD];
+  __shared__ float ml[NW][16][2];
+
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int n = lane & 15, g = lane >> 4;
+  int unit = blockIdx.x / a.S;
+  const int split = blockIdx.x - unit * a.S;
+  // Rows next to each other (SPARSE) and the head tiles of a group read the
+  // same pages: give each XCD (workgroup id mod 8) one run of them.
+  if (SPARSE || a.MT > 1) {
+    const int per = (units + 7) >> 3;
+    unit = (unit & 7) * per + (unit >> 3);
+    if (unit >= units) return;
+  }
+  const int mt = unit % a.MT;
+  const int rh = unit / a.MT;
+  const int h = rh / a.R, row = rh - h * a.R;
+  const int req = a.row_req == nullptr ? row : a.row_req[row];
+  const int P = 1 << a.lp;
+  int len = min(a.row_len[row], a.max_len);
+  if (req < 0 || req >= a.B) len = 0;
+  const int heads = min(16, a.G - 16 * mt);      // of this tile
+  const int head0 = h * a.G + 16 * mt;
+  const int32_t* table = a.table + (size_t)(len > 0 ? req : 0) * a.W;
+  const int32_t* list = SPARSE ? a.blocks + ((size_t)row * a.Hkv + h) * a.n_blocks : nullptr;
+  const int vkeys = len <= 0 ? 0 : SPARSE ? a.n_blocks << a.lp : len;   // < 2^31: 4096 * 128
+  const int nt = (int)(((int64_t)vkeys + KT - 1) / KT);
+  const int t0 = (int)((int64_t)nt * split / a.S) + wave, t1 = (int)((int64_t)nt * (split + 1) / a.S);
+  const E* kc = static_cast<const E*>(a.kc);
+  const E* vc = static_cast<const E*>(a.vc);
+
+  frag_t<E> qf[NS];
+  {
+    const E* q = static_cast<const E*>(a.q) + row * a.ldq + (size_t)(head0 + n) * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[s] = n < heads ? ld8a(q + 32 * s) : zero_frag<E>();
+  }
+
+  // Lane l looks up half l % 2 of this wave's tile number l / 2 (of the next
+  // 32); the loop reads the answers lane by lane.
+  int pg = 0, at = 0, cnt = 0;
+  auto look_up = [&](int t) {
+    const int tile = t + NW * (lane >> 1);
+    const int64_t vk = (int64_t)tile * KT + 16 * (lane & 1);
+    cnt = 0; pg = 0; at = 0;
+    if (tile < t1 && vk < vkeys) {
+      int j = (int)vk >> a.lp;
+      at = (int)vk & (P - 1);
+      bool ok = true;
+      if (SPARSE) {
+        j = list[j];
+        ok = j >= 0 && j <= (len - 1) >> a.lp;
+      }
+      if (ok) {
+        const int page = table[j];
+        if (page >= 0 && page < a.n_pages) {
+          pg = page;
+          cnt = min(max(len - ((j << a.lp) + at), 0), 16);
+        }
+      }
+    }
+    if (cnt == 0) { pg = 0; at = 0; }   // a place that can be read: page 0
+  };
+  auto half = [&](int i) {              // i: lane that looked it up
+    const int p = __builtin_amdgcn_readlane(pg, i), o = __builtin_amdgcn_readlane(at, i);
+    return Half{((size_t)p * a.Hkv + h) * P + o, __builtin_amdgcn_readlane(cnt, i)};
+  };
+
+  frag_t<E> kf[2][NS];
+  uint32_t vf[8][DW];
+  auto load_k = [&](const Half& h0, const Half& h1) {
+    const E* p = kc + (n < 8 ? h0.row : h1.row) * D + ((8 * (n >> 2) + (n & 3)) & 15) * D + 8 * g;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) kf[t][s] = ld8a(p + 4 * t * D + 32 * s);
+  };
+  auto load_v = [&](const Half& h0, const Half& h1) {
+    const E* p = vc + (g < 2 ? h0.row : h1.row) * D + (size_t)(8 * (g & 1)) * D + n * EPL;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (DW == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + j * D);
+        vf[j][0] = x.x; vf[j][1] = x.y;
+      } else {
+#pragma unroll
+        for (int w = 0; w < DW / 4; ++w) {
+          const V16 x = ldv(p + j * D + w * (16 / (int)sizeof(E)));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) vf[j][4 * w + u] = x.w[u];
+        }
+      }
+    }
+  };
+
+  float c = -INFINITY, l = 0.f;       // reference and (this lane's part of the) sum of head n
+  bool seen = false;                  // uniform: some key took part
+  f32x4 acc[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) acc[i] = zero4();
+
+  int slot = 0;                       // lane of the current tile's look-up
+  look_up(t0);
+  Half h0 = half(0), h1 = half(1);
+  if (t0 < t1) { load_k(h0, h1); load_v(h0, h1); }
+  for (int t = t0; t < t1; t += NW) {
+    f32x4 s0 = zero4(), s1 = zero4();
+#pragma unroll
+    for (int s = 0; s < NS; ++s) { s0 = mma(kf[0][s], qf[s], s0); s1 = mma(kf[1][s], qf[s], s1); }
+    const Half c0 = h0, c1 = h1;
+    slot += 2;
+    const bool more = t + NW < t1;
+    if (more) {
+      if (slot == 64) { look_up(t + NW); slot = 0; }
+      h0 = half(slot);
+      h1 = half(slot + 1);
+      load_k(h0, h1);
+    }
+    const bool some = c0.n + c1.n > 0;
+    if (some) {
+      seen = true;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { x[j] = s0[j] * a.scale; x[4 + j] = s1[j] * a.scale; }
+      if (c0.n + c1.n < 32) {
+        const int live = (g < 2 ? c0.n : c1.n) - 8 * (g & 1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= live) {
+            x[j] = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < DW; ++w) vf[j][w] = 0u;    // 0 * NaN would reach the sum
+          }
+        }
+      }
+      float mx = x[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) mx = fmaxf(mx, x[j]);
+      if (__ballot(mx > c + (BIAS + 4.f)) != 0ull) {
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        const float cn = fmaxf(c, mx - BIAS);
+        const float f = cn == -INFINITY ? 1.f : exp2f(c - cn);
+        c = cn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) acc[i] *= f;
+      }
+      const float cs = c == -INFINITY ? 0.f : c;           // every x so far is -inf
+      f32x8 p;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) { p[j] = exp2f(x[j] - cs); l += p[j]; }
+      frag_t<E> ph, pl;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ph[j] = from_f<E>(p[j]);
+        if (TWO) pl[j] = from_f<E>(p[j] - to_f(ph[j]));
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const frag_t<E> vt = v_frag<E, DW>(vf, i);
+        acc[i] = mma(vt, ph, acc[i]);
+        if (TWO) acc[i] = mma(vt, pl, acc[i]);
+      }
+    }
+    if (more) load_v(h0, h1);
+  }
+
+  // join the four waves
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (g == 0) { ml[wave][n][0] = c; ml[wave][n][1] = seen ? l : -1.f; }
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][n][0]);
+  const float mine = c == -INFINITY ? 0.f : exp2f(c - top);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4)
+      st4f(&joined[wave][n][(4 * g + j) * EPL + i],
+           f32x4{acc[i][j] * mine, acc[i + 1][j] * mine, acc[i + 2][j] * mine, acc[i + 3][j] * mine});
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * (D / 4); i += 64 * NW) {
+    const int hd = i / (D / 4), e = 4 * (i % (D / 4));
+    float m = -INFINITY, sum = 0.f;
+    bool any = false;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, ml[w][hd][0]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float lw = ml[w][hd][1], cw = ml[w][hd][0];
+      any = any || !(lw == -1.f);
+      if (cw != -INFINITY) sum += lw * exp2f(cw - m);
+      else if (!(lw <= 0.f)) sum = lw;                     // NaN
+    }
+    f32x4 o = zero4();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) o += *reinterpret_cast<const f32x4*>(&joined[w][hd][e]);
+    const size_t rq = (size_t)row * a.Hq + head0 + hd;
+    if (a.S > 1) {
+      const size_t to = rq * a.S + split;
+      st4f(a.part_o + to * D + e, o);
+      if (e == 0) { a.part_ml[2 * to] = m; a.part_ml[2 * to + 1] = any ? sum : -1.f; }
+    } else {
+      if (any) o /= sum;
+      st4o(static_cast<O*>(a.o) + rq * D + e, o);
+      if (a.lse != nullptr && e == 0)
+        a.lse[rq] = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+}
+
+// Joins the S splits of a (row, query head).  A wave reads every fourth split.
+template <typename O, int D>
+__global__ __launch_bounds__(256) void join_kernel(PageAttendArgs a) {
+  constexpr int PER = D / 64;
+  __shared__ float joined[4][D];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const size_t rq = blockIdx.x;
+  const float* ml = a.part_ml + rq * a.S * 2;
+  float m = -INFINITY;
+  for (int s = lane; s < a.S; s += 64) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  float sum = 0.f;
+  bool any = false;
+  for (int s = lane; s < a.S; s += 64) {
+    const float lw = ml[2 * s + 1], cw = ml[2 * s];
+    any = any || !(lw == -1.f);
+    if (cw != -INFINITY) sum += lw * exp2f(cw - m);
+    else if (!(lw <= 0.f)) sum += lw;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+  any = __ballot(any) != 0ull;
+  float acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  const float* p = a.part_o + rq * a.S * D + lane * PER;
+#pragma unroll 4
+  for (int s = wave; s < a.S; s += 4) {
+    const float cw = ml[2 * s];
+    const float w = cw == -INFINITY ? 0.f : exp2f(cw - m);
+    if (w != 0.f) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += w * p[(size_t)s * D + i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) joined[wave][lane * PER + i] = acc[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < D; e += 256) {
+    float o = (joined[0][e] + joined[1][e]) + (joined[2][e] + joined[3][e]);
+    if (any) o /= sum;
+    static_cast<O*>(a.o)[rq * D + e] = from_f<O>(o);
+  }
+  if (a.lse != nullptr && threadIdx.x == 0)
+    a.lse[rq] = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <typename E, typename O, int D> hipError_t launch_d(const PageAttendArgs& a, hipStream_t s) {
+  const int units = a.R * a.Hkv * a.MT;
+  const unsigned grid = (unsigned)((a.blocks != nullptr || a.MT > 1 ? (units + 7) / 8 * 8 : units) * a.S);
+  if (a.blocks != nullptr)
+    hipLaunchKernelGGL((attend_kernel<E, O, D, true>), dim3(grid), dim3(64 * NW), 0, s, a, units);
+  else
+    hipLaunchKernelGGL((attend_kernel<E, O, D, false>), dim3(grid), dim3(64 * NW), 0, s, a, units);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.S == 1) return e;
+  hipLaunchKernelGGL((join_kernel<O, D>), dim3((unsigned)(a.R * a.Hq)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename E, typename O> hipError_t launch_o(const PageAttendArgs& a, int d, hipStream_t s) {
+  if (d == 64) return launch_d<E, O, 64>(a, s);
+  if (d == 128) return launch_d<E, O, 128>(a, s);
+  return launch_d<E, O, 256>(a, s);
+}
+
+template <typename E> hipError_t launch_e(const PageAttendArgs& a, int o_dtype, int d, hipStream_t s) {
+  if (o_dtype == 1) return launch_o<E, bf16>(a, d, s);
+  if (o_dtype == 2) return launch_o<E, fp16>(a, d, s);
+  return launch_o<E, float>(a, d, s);
+}
+
+}  // namespace
+
+// Splits of each unit's keys: enough workgroups to keep every CU's memory
+// pipeline busy (4 per CU), but at least two tiles for each wave of one.
+int paged_splits(long long units, int tiles) {
+  const long long want = (1024 + units - 1) / units;
+  const long long most = (tiles + 2 * NW - 1) / (2 * NW);
+  const long long s = want < most ? want : most;
+  return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+
+hipError_t launch_paged_attend(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {
+  if (dtype == 1) return launch_e<bf16>(a, o_dtype, d, s);
+  if (dtype == 2) return launch_e<fp16>(a, o_dtype, d, s);
+  return launch_e<float>(a, o_dtype, d, s);
+}
+
+}  // namespace sgdn

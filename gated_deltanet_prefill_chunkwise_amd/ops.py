@@ -1,4 +1,5 @@
-"""Thin Python binding of libsgdn.so (C ABI in include/sgdn.h).
+"""Thin Python binding of libsgdn.so (C ABI in include/sgdn.h and, for the
+paged attention operators ``paged_*``, include/sgdn_attn.h).
 
 Argument marshalling only: every step of the prefill runs in the library's HIP
 kernels.  Tensors are torch device tensors (torch provides memory and the
@@ -16,7 +17,10 @@ SGDN_F32, SGDN_BF16, SGDN_F16 = 0, 1, 2
 SOLVES = {"exact": 0, "blockadj": 1}
 EXPORTS = ("sgdn_workspace_bytes", "sgdn_event_capacity", "sgdn_prefill_dense", "sgdn_select",
            "sgdn_prefill_sparse", "sgdn_decode_step", "sgdn_status_string", "sgdn_fp64_selftest",
-           "sgdn_select_noalloc")
+           "sgdn_select_noalloc",
+           "sgdn_paged_release", "sgdn_paged_plan", "sgdn_paged_write",
+           "sgdn_paged_workspace_bytes", "sgdn_paged_attend", "sgdn_paged_attend_sparse",
+           "sgdn_paged_select")
 NOALLOC_SCRATCH_BYTES = 4 << 20   # SGDN_NOALLOC_SCRATCH_BYTES
 
 
@@ -44,6 +48,12 @@ class Stats(ctypes.Structure):
                 ("n_tier", ctypes.c_int32 * 3), ("k", ctypes.c_int32 * 3),
                 ("n_snapshots", ctypes.c_int32), ("nonfinite_input", ctypes.c_int32),
                 ("nonfinite_output", ctypes.c_int32)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "batch", "n_q", "n_kv", "d", "page", "n_pages", "width", "max_len",
+                 "dtype", "o_dtype")]
 
 
 # bits of Stats.nonfinite_input / nonfinite_output (SGDN_NF_*)
@@ -103,6 +113,19 @@ def lib():
         L.sgdn_prefill_sparse.restype = i32
         L.sgdn_decode_step.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.sgdn_decode_step.restype = i32
+        PG, f32, i64 = ctypes.POINTER(Paged), ctypes.c_float, ctypes.c_int64
+        L.sgdn_paged_release.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.sgdn_paged_plan.argtypes = [i32, i32, i32, i32, i32] + [vp] * 14
+        L.sgdn_paged_write.argtypes = [PG, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp]
+        L.sgdn_paged_workspace_bytes.argtypes = [PG, i32, i32]
+        L.sgdn_paged_workspace_bytes.restype = sz
+        L.sgdn_paged_attend.argtypes = [PG, vp, i64, vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp]
+        L.sgdn_paged_attend_sparse.argtypes = [PG, vp, i64, vp, vp, vp, vp, vp, vp, i32, f32, vp,
+                                               vp, vp, sz, vp]
+        L.sgdn_paged_select.argtypes = [PG, vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, sz,
+                                        vp]
+        for name in ("release", "plan", "write", "attend", "attend_sparse", "select"):
+            getattr(L, "sgdn_paged_" + name).restype = i32
         L.sgdn_status_string.argtypes = [i32]
         L.sgdn_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -477,3 +500,348 @@ def prefill_sparse(q, k, v, a, beta, z=None, keep_budget=0.29, solve="blockadj",
         raise SgdnError(st, "sgdn_prefill_sparse")
     return o, s_final, stats
 
+
+
+# Paged attention (include/sgdn_attn.h) ---------------------------------------
+#
+# The tensors of a call must share one device, which need not be the current
+# one; ``stream`` is a stream of that device (default: its current stream).  On
+# another stream than the current one a call allocates from that stream's
+# memory and holds the tensors that it is given for it (``record_stream``).
+
+PLAN_REFUSED = {"pages": 1, "width": 2, "rows": 4, "negative": 8}   # codes of paged_plan's status
+
+
+class _On:
+    """The call's device as the current one, and its stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.stream = self.current = torch.cuda.current_stream(device)
+        self.other = stream is not None and stream != self.current
+        if self.other:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.stream = stream
+        self.device = device
+        self.away = device.index != torch.cuda.current_device()
+
+    def empty(self, shape, dtype):
+        """Memory that belongs to the call's stream, held for the current one too."""
+        import torch
+        if not self.other:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(self.current)
+        return t
+
+    def call(self, name, *args, hold=()):
+        fn = getattr(lib(), name)
+        if self.away:
+            import torch
+            with torch.cuda.device(self.device):
+                st = fn(*args, self.stream.cuda_stream)
+        else:
+            st = fn(*args, self.stream.cuda_stream)
+        if st != 0:
+            raise SgdnError(st, name)
+        if self.other:
+            for t in hold:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _dev_check(device, **tensors):
+    """Contiguous device tensors of one device; a name ending in a type's letter
+    (``_i``, ``_l``, ``_f``, ``_b``, ``_u``) asks for that element type."""
+    import torch
+    kinds = {"_i": torch.int32, "_l": torch.int64, "_f": torch.float32, "_b": torch.int8,
+             "_u": torch.uint8}
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        dtype = kinds.get(name[-2:])
+        if dtype is not None:
+            name = name[:-2]
+        _check(t, name, dtype)
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _shape_check(name, t, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _row_view(t, name, device, dtype):
+    """[R, heads, d] whose rows are contiguous; returns its row stride."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, heads, d = t.shape
+    ld, sh, se = t.stride()
+    if rows > 1 and ld < heads * d or (heads > 1 and sh != d) or (d > 1 and se != 1):
+        raise ValueError(f"each row of {name} must be contiguous, got strides {t.stride()}")
+    return ld if rows > 1 else heads * d
+
+
+def _paged(rows, q_heads, cache_shape, dtype, out_dtype=None, batch=1, width=1, max_len=None):
+    n_pages, n_kv, page, d = cache_shape
+    return Paged(rows, batch, q_heads, n_kv, d, page, n_pages, width,
+                 0 if max_len is None else int(max_len), _ocode(dtype),
+                 _ocode(dtype if out_dtype is None else out_dtype))
+
+
+def paged_workspace_bytes(shape: Paged, n_blocks=0, select=False) -> int:
+    """Workspace of paged_attend (``n_blocks`` 0), paged_attend_sparse or paged_select."""
+    return int(lib().sgdn_paged_workspace_bytes(ctypes.byref(shape), int(n_blocks), int(select)))
+
+
+def _paged_ws(shape, n_blocks, select, on, workspace):
+    nbytes = paged_workspace_bytes(shape, n_blocks, select)
+    if nbytes == 0:
+        raise SgdnError(-2, "sgdn_paged_workspace_bytes")
+    if workspace is not None:
+        _dev_check(on.device, workspace=workspace)
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise SgdnError(-3, "workspace")
+        return workspace, workspace.numel() * workspace.element_size()
+    import torch
+    return on.empty(nbytes, torch.uint8), nbytes
+
+
+def paged_release(lens, done, table, free_list, free_pos, page, lens_out=None, free_pos_out=None,
+                  stream=None):
+    """Pages of ended requests back to the ring; returns (lens, free_pos).
+
+    ``done`` uint8 [B]; ``free_list`` int32 [n_free] is updated in place;
+    ``lens_out`` / ``free_pos_out`` may be ``lens`` / ``free_pos`` themselves
+    (updated in place), by default new tensors.
+    """
+    import torch
+    dev = lens.device
+    _dev_check(dev, lens_i=lens, done_u=done, table_i=table, free_list_i=free_list,
+               free_pos_l=free_pos, lens_out_i=lens_out, free_pos_out_l=free_pos_out)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, W]")
+    B, W = table.shape
+    on = _On(dev, stream)
+    if lens_out is None:
+        lens_out = on.empty((B,), torch.int32)
+    if free_pos_out is None:
+        free_pos_out = on.empty((2,), torch.int64)
+    for n, t, shape in (("lens", lens, (B,)), ("done", done, (B,)), ("free_pos", free_pos, (2,)),
+                        ("lens_out", lens_out, (B,)), ("free_pos_out", free_pos_out, (2,))):
+        _shape_check(n, t, shape)
+    on.call(
+        "sgdn_paged_release", B, page, W, free_list.numel(), lens.data_ptr(), done.data_ptr(),
+        table.data_ptr(), free_list.data_ptr(), free_pos.data_ptr(), lens_out.data_ptr(),
+        free_pos_out.data_ptr(),
+        hold=(lens, done, table, free_list, free_pos, lens_out, free_pos_out))
+    return lens_out, free_pos_out
+
+
+def paged_plan(lens, add, table, free_list, free_pos, page, rows, lens_out=None,
+               free_pos_out=None, out=None, stream=None):
+    """Pages, slots and row descriptors of a step's new tokens; returns a dict.
+
+    ``table`` int32 [B, W] gets the new pages in place.  The dict holds lens,
+    free_pos, cu and page_cu [B + 1], slot, row_req and row_len [rows] and
+    status [B] (0, or why a request was refused: ``PLAN_REFUSED``).
+    ``lens_out`` / ``free_pos_out`` may be ``lens`` / ``free_pos`` themselves;
+    ``out`` reuses the dict of an earlier call of the same sizes.
+    """
+    import torch
+    dev = lens.device
+    _dev_check(dev, lens_i=lens, add_i=add, table_i=table, free_list_i=free_list,
+               free_pos_l=free_pos, lens_out_i=lens_out, free_pos_out_l=free_pos_out)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, W]")
+    B, W = table.shape
+    rows = int(rows)
+    if rows < 0:
+        raise ValueError(f"rows must not be negative, got {rows}")
+    on = _On(dev, stream)
+    sizes = dict(cu=B + 1, page_cu=B + 1, slot=rows, row_req=rows, row_len=rows, status=B)
+    if out is None:
+        own = on.empty((sum(sizes.values()) + B,), torch.int32)
+        parts = own.split([*sizes.values(), B])
+        out = dict(zip(sizes, parts))
+        out["lens"] = parts[-1] if lens_out is None else lens_out
+        out["free_pos"] = on.empty((2,), torch.int64) if free_pos_out is None else free_pos_out
+    else:
+        out = dict(out)
+        for n, size in sizes.items():
+            _dev_check(dev, **{n + "_i": out[n]})
+            _shape_check(n, out[n], (size,))
+        if lens_out is not None:
+            out["lens"] = lens_out
+        if free_pos_out is not None:
+            out["free_pos"] = free_pos_out
+        _dev_check(dev, lens_i=out["lens"], free_pos_l=out["free_pos"])
+    for n, t, shape in (("lens", lens, (B,)), ("add", add, (B,)), ("free_pos", free_pos, (2,)),
+                        ("lens_out", out["lens"], (B,)), ("free_pos_out", out["free_pos"], (2,))):
+        _shape_check(n, t, shape)
+    o = out
+    on.call(
+        "sgdn_paged_plan", B, page, W, rows, free_list.numel(), lens.data_ptr(), add.data_ptr(),
+        table.data_ptr(), free_list.data_ptr(), free_pos.data_ptr(), o["lens"].data_ptr(),
+        o["free_pos"].data_ptr(), o["cu"].data_ptr(), o["page_cu"].data_ptr(),
+        o["slot"].data_ptr(), o["row_req"].data_ptr(), o["row_len"].data_ptr(),
+        o["status"].data_ptr(),
+        hold=(lens, add, table, free_list, free_pos, *o.values()))
+    return out
+
+
+def paged_write(k, v, slot, k_cache, v_cache, codes=None, code_scale=None, stream=None):
+    """New keys and values [R, Hkv, d] into their slots, in place.
+
+    k and v may be views with a row stride (a joint projection's output).
+    With ``codes`` int8 [n_pages, Hkv, d] and ``code_scale`` fp32
+    [n_pages, Hkv] the pages that the rows complete are summarised there, for
+    ``paged_select``.
+    """
+    dev, dt = k_cache.device, k_cache.dtype
+    _dev_check(dev, slot_i=slot, k_cache=k_cache, v_cache=v_cache, codes_b=codes,
+               code_scale_f=code_scale)
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [n_pages, Hkv, page, d]")
+    ldk, ldv = _row_view(k, "k", dev, dt), _row_view(v, "v", dev, dt)
+    n_pages, n_kv, page, d = k_cache.shape
+    rows = k.shape[0]
+    if v_cache.dtype != dt:
+        raise ValueError(f"v_cache must be {dt}, got {v_cache.dtype}")
+    for n, t, shape in (("v_cache", v_cache, (n_pages, n_kv, page, d)), ("k", k, (rows, n_kv, d)),
+                        ("v", v, (rows, n_kv, d)), ("slot", slot, (rows,)),
+                        ("codes", codes, (n_pages, n_kv, d)),
+                        ("code_scale", code_scale, (n_pages, n_kv))):
+        _shape_check(n, t, shape)
+    shape = _paged(rows, n_kv, (n_pages, n_kv, page, d), dt)
+    _On(dev, stream).call(
+        "sgdn_paged_write", ctypes.byref(shape), k.data_ptr(), v.data_ptr(), ldk, ldv,
+        slot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        None if codes is None else codes.data_ptr(),
+        None if code_scale is None else code_scale.data_ptr(),
+        hold=(k, v, slot, k_cache, v_cache, codes, code_scale))
+
+
+def _paged_rows(q, table, row_len, row_req, dev):
+    """Checks what the reading calls share; returns (rows, batch, width)."""
+    _dev_check(dev, table_i=table, row_len_i=row_len, row_req_i=row_req)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, W]")
+    rows = q.shape[0]
+    _shape_check("row_len", row_len, (rows,))
+    _shape_check("row_req", row_req, (rows,))
+    if row_req is None and rows > table.shape[0]:
+        raise ValueError("without row_req, row r is request r: more rows than requests")
+    return rows, table.shape[0], table.shape[1]
+
+
+def _attend(name, q, k_cache, v_cache, table, row_len, row_req, blocks, scale, max_len, o,
+            out_dtype, want_lse, lse, workspace, stream):
+    import torch
+    dev, dt = k_cache.device, k_cache.dtype
+    ldq = _row_view(q, "q", dev, dt)
+    if o is not None:
+        out_dtype = o.dtype
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    _dev_check(dev, k_cache=k_cache, v_cache=v_cache, blocks_i=blocks, o=o, lse_f=lse)
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [n_pages, Hkv, page, d]")
+    if v_cache.dtype != dt:
+        raise ValueError(f"v_cache must be {dt}, got {v_cache.dtype}")
+    _shape_check("v_cache", v_cache, tuple(k_cache.shape))
+    rows, B, W = _paged_rows(q, table, row_len, row_req, dev)
+    n_q, d = q.shape[1], q.shape[2]
+    if d != k_cache.shape[3]:
+        raise ValueError(f"q has heads of {d}, the cache of {k_cache.shape[3]}")
+    _shape_check("o", o, (rows, n_q, d))
+    _shape_check("lse", lse, (rows, n_q))
+    n_blocks = 0
+    if blocks is not None:
+        if blocks.dim() != 3 or blocks.shape[2] < 1:
+            raise ValueError("blocks must be [R, Hkv, n_blocks]")
+        n_blocks = blocks.shape[2]
+        _shape_check("blocks", blocks, (rows, k_cache.shape[1], n_blocks))
+    shape = _paged(rows, n_q, k_cache.shape, dt, out_dtype, B, W, max_len)
+    on = _On(dev, stream)
+    ws, nbytes = _paged_ws(shape, n_blocks, False, on, workspace)
+    if o is None:
+        o = on.empty((rows, n_q, d), out_dtype)
+    if want_lse and lse is None:
+        lse = on.empty((rows, n_q), torch.float32)
+    if scale is None:
+        scale = d ** -0.5
+    lists = () if blocks is None else (blocks.data_ptr(), n_blocks)
+    on.call(name, ctypes.byref(shape), q.data_ptr(), ldq, k_cache.data_ptr(), v_cache.data_ptr(),
+            table.data_ptr(), None if row_req is None else row_req.data_ptr(),
+            row_len.data_ptr(), *lists, float(scale), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), nbytes,
+            hold=(q, k_cache, v_cache, table, row_req, row_len, blocks, o, lse, ws))
+    return o, lse
+
+
+def paged_attend(q, k_cache, v_cache, table, row_len, row_req=None, scale=None, max_len=None,
+                 o=None, out_dtype=None, want_lse=False, lse=None, workspace=None, stream=None):
+    """Attention of rows [R, Hq, d] over their whole cached sequence; returns (o, lse).
+
+    Row r belongs to request ``row_req[r]`` (by default r) and sees its first
+    ``row_len[r]`` tokens; rows that see nothing give 0 (lse -inf).  ``scale``
+    is d**-0.5 by default, o fp32 unless ``out_dtype`` (or a given ``o``) says
+    otherwise, lse None unless asked for.  ``max_len``: an upper bound of
+    ``row_len`` that is known on the host (by default what the table holds;
+    longer rows are cut to it): the work is split by it.
+    """
+    return _attend("sgdn_paged_attend", q, k_cache, v_cache, table, row_len, row_req, None, scale,
+                   max_len, o, out_dtype, want_lse, lse, workspace, stream)
+
+
+def paged_attend_sparse(q, k_cache, v_cache, table, row_len, blocks, row_req=None, scale=None,
+                        max_len=None, o=None, out_dtype=None, want_lse=False, lse=None,
+                        workspace=None, stream=None):
+    """``paged_attend`` over the blocks listed in ``blocks`` int32
+    [R, Hkv, n_blocks] only (-1: none), as ``paged_select`` returns them."""
+    if blocks is None:
+        raise ValueError("blocks must be given")
+    return _attend("sgdn_paged_attend_sparse", q, k_cache, v_cache, table, row_len, row_req,
+                   blocks, scale, max_len, o, out_dtype, want_lse, lse, workspace, stream)
+
+
+def paged_select(q, codes, code_scale, table, row_len, page, n_blocks, row_req=None, n_sink=1,
+                 n_local=1, max_len=None, blocks=None, workspace=None, stream=None):
+    """The ``n_blocks`` blocks that each row and key/value head reads; returns
+    int32 [R, Hkv, n_blocks], rising, -1 behind the last.
+
+    ``codes`` and ``code_scale`` are the page summaries of ``paged_write``.  A
+    row's first ``n_sink`` and last ``n_local`` blocks are always among them.
+    """
+    import torch
+    dev = codes.device
+    _dev_check(dev, codes_b=codes, code_scale_f=code_scale, blocks_i=blocks)
+    if codes.dim() != 3:
+        raise ValueError("codes must be [n_pages, Hkv, d]")
+    n_pages, n_kv, d = codes.shape
+    _shape_check("code_scale", code_scale, (n_pages, n_kv))
+    ldq = _row_view(q, "q", dev, q.dtype)
+    rows, B, W = _paged_rows(q, table, row_len, row_req, dev)
+    if q.shape[2] != d:
+        raise ValueError(f"q has heads of {q.shape[2]}, the summaries of {d}")
+    _shape_check("blocks", blocks, (rows, n_kv, n_blocks))
+    shape = _paged(rows, q.shape[1], (n_pages, n_kv, page, d), q.dtype, None, B, W, max_len)
+    on = _On(dev, stream)
+    ws, nbytes = _paged_ws(shape, n_blocks, True, on, workspace)
+    if blocks is None:
+        blocks = on.empty((rows, n_kv, n_blocks), torch.int32)
+    on.call("sgdn_paged_select", ctypes.byref(shape), q.data_ptr(), ldq, codes.data_ptr(),
+            code_scale.data_ptr(), table.data_ptr(),
+            None if row_req is None else row_req.data_ptr(), row_len.data_ptr(), n_blocks, n_sink,
+            n_local, blocks.data_ptr(), ws.data_ptr(), nbytes,
+            hold=(q, codes, code_scale, table, row_req, row_len, blocks, ws))
+    return blocks

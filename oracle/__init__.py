@@ -20,6 +20,8 @@ Modules
   detfp    fixed-order fp64 helpers that make selector decisions reproducible
   selector tail score, gate energy, tier budgets, dynamic selector, CSR
            event layout (Eqs. 9-16)
+  paged    paged softmax attention beside the linear layers: page bookkeeping,
+           cache write and page summaries, attention, block choice
   sparse   deferred W, event-sparse H, two-chunk grouped O, end-to-end sparse
            prefill (Eqs. 15, 17-25)
 
@@ -31,4 +33,4 @@ invariants, and the end-to-end sparse outputs are pinned through the
 all-events-kept fixed point and the Eq. (25) identity.
 """
 
-from . import detfp, gdn, selector, sparse  # noqa: F401
+from . import detfp, gdn, paged, selector, sparse  # noqa: F401
