@@ -85,7 +85,8 @@ struct PageSelectArgs {
 hipError_t launch_paged_release(const ReleaseArgs& a, hipStream_t s);
 hipError_t launch_paged_plan(const PagePlanArgs& a, hipStream_t s);
 hipError_t launch_paged_write(const PageWriteArgs& a, int dtype, int d, hipStream_t s);
-int paged_splits(long long units, int tiles);   // S of PageAttendArgs
+// S of PageAttendArgs: `units` (row, head, head tile), `tiles` of 32 keys, bytes of a key row
+int paged_splits(long long units, int tiles, int row_bytes);
 hipError_t launch_paged_attend(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 hipError_t launch_paged_select(const PageSelectArgs& a, int dtype, int d, hipStream_t s);
 

@@ -67,7 +67,8 @@ AttendPlan attend_plan(const sgdn_paged* p, int n_blocks) {
   const int G = p->n_q / p->n_kv;
   pl.MT = (G + 15) / 16;
   const int64_t keys = n_blocks > 0 ? (int64_t)n_blocks * p->page : longest(p);
-  pl.S = p->rows > 0 ? paged_splits((long long)p->rows * p->n_kv * pl.MT, (int)((keys + 31) / 32)) : 1;
+  pl.S = p->rows > 0 ? paged_splits((long long)p->rows * p->n_kv * pl.MT, (int)((keys + 31) / 32),
+                                     p->d * (p->dtype == SGDN_F32 ? 4 : 2)) : 1;
   pl.off_ml = pl.total = 0;
   if (pl.S > 1) {
     const size_t parts = (size_t)p->rows * p->n_q * pl.S;

@@ -37,6 +37,7 @@ namespace {
 
 constexpr int NW = 4;        // waves of a workgroup
 constexpr int KT = 32;       // keys of a tile
+constexpr int MAX_SPLITS = 256;
 
 template <typename E> struct Bias { static constexpr float V = 0.f; };
 template <> struct Bias<fp16> { static constexpr float V = 10.f; };
@@ -293,52 +294,62 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
   }
 }
 
-// Joins the S splits of a (row, query head).  A wave reads every fourth split.
+// Joins the S <= 256 splits of 64 elements of a (row, query head): thread t
+// sums elements 4 (t % 16) .. of the splits t / 16 + 16 i.
 template <typename O, int D>
 __global__ __launch_bounds__(256) void join_kernel(PageAttendArgs a) {
-  constexpr int PER = D / 64;
-  __shared__ float joined[4][D];
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const size_t rq = blockIdx.x;
-  const float* ml = a.part_ml + rq * a.S * 2;
-  float m = -INFINITY;
-  for (int s = lane; s < a.S; s += 64) m = fmaxf(m, ml[2 * s]);
+  __shared__ float weight[MAX_SPLITS];
+  __shared__ f32x4 joined[4][16];
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
+  const size_t rq = blockIdx.x / (D / 64);
+  const int e0 = (int)(blockIdx.x % (D / 64)) * 64 + 4 * (lane & 15);
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + rq * a.S;
+  // every wave makes the maximum and the sum for itself
+  float c[MAX_SPLITS / 64], l[MAX_SPLITS / 64], m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < MAX_SPLITS / 64; ++i) {
+    const int s = 64 * i + lane;
+    const float2 x = s < a.S ? ml[s] : float2{-INFINITY, -1.f};
+    c[i] = x.x;
+    l[i] = x.y;
+    m = fmaxf(m, x.x);
+  }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   float sum = 0.f;
   bool any = false;
-  for (int s = lane; s < a.S; s += 64) {
-    const float lw = ml[2 * s + 1], cw = ml[2 * s];
-    any = any || !(lw == -1.f);
-    if (cw != -INFINITY) sum += lw * exp2f(cw - m);
-    else if (!(lw <= 0.f)) sum += lw;
+#pragma unroll
+  for (int i = 0; i < MAX_SPLITS / 64; ++i) {
+    any = any || !(l[i] == -1.f);
+    const float w = c[i] == -INFINITY ? 0.f : exp2f(c[i] - m);
+    if (c[i] != -INFINITY) sum += l[i] * w;
+    else if (!(l[i] <= 0.f)) sum += l[i];                  // NaN
+    if (wave == 0) weight[64 * i + lane] = w;
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
   any = __ballot(any) != 0ull;
-  float acc[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  const float* p = a.part_o + rq * a.S * D + lane * PER;
-#pragma unroll 4
-  for (int s = wave; s < a.S; s += 4) {
-    const float cw = ml[2 * s];
-    const float w = cw == -INFINITY ? 0.f : exp2f(cw - m);
-    if (w != 0.f) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += w * p[(size_t)s * D + i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) joined[wave][lane * PER + i] = acc[i];
   __syncthreads();
-  for (int e = threadIdx.x; e < D; e += 256) {
-    float o = (joined[0][e] + joined[1][e]) + (joined[2][e] + joined[3][e]);
-    if (any) o /= sum;
-    static_cast<O*>(a.o)[rq * D + e] = from_f<O>(o);
+  const float* p = a.part_o + rq * a.S * D + e0;
+  f32x4 acc = zero4();
+#pragma unroll 4
+  for (int s = tid >> 4; s < a.S; s += 16) {
+    const float w = weight[s];
+    if (w != 0.f) acc += w * *reinterpret_cast<const f32x4*>(p + (size_t)s * D);
   }
-  if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[rq] = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o, 64);
+  if (lane < 16) joined[wave][lane] = acc;
+  __syncthreads();
+  if (tid < 16) {
+    f32x4 o = (joined[0][tid] + joined[1][tid]) + (joined[2][tid] + joined[3][tid]);
+    if (any) o /= sum;
+    st4o(static_cast<O*>(a.o) + rq * D + e0, o);
+    if (a.lse != nullptr && e0 == 0)
+      a.lse[rq] = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
 template <typename E, typename O, int D> hipError_t launch_d(const PageAttendArgs& a, hipStream_t s) {
@@ -350,7 +361,7 @@ template <typename E, typename O, int D> hipError_t launch_d(const PageAttendArg
     hipLaunchKernelGGL((attend_kernel<E, O, D, false>), dim3(grid), dim3(64 * NW), 0, s, a, units);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.S == 1) return e;
-  hipLaunchKernelGGL((join_kernel<O, D>), dim3((unsigned)(a.R * a.Hq)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((join_kernel<O, D>), dim3((unsigned)(a.R * a.Hq * (D / 64))), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -368,13 +379,14 @@ template <typename E> hipError_t launch_e(const PageAttendArgs& a, int o_dtype, 
 
 }  // namespace
 
-// Splits of each unit's keys: enough workgroups to keep every CU's memory
-// pipeline busy (4 per CU), but at least two tiles for each wave of one.
-int paged_splits(long long units, int tiles) {
-  const long long want = (1024 + units - 1) / units;
-  const long long most = (tiles + 2 * NW - 1) / (2 * NW);
+// Splits of each unit's keys: `groups` workgroups to keep every CU's memory
+// pipeline busy, but a tile at least for each wave of one.
+int paged_splits(long long units, int tiles, int row_bytes) {
+  const int groups = row_bytes >= 512 ? 512 : 1024;
+  const long long want = (groups + units - 1) / units;
+  const long long most = (tiles + NW - 1) / NW;
   const long long s = want < most ? want : most;
-  return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+  return (int)(s < 1 ? 1 : s > MAX_SPLITS ? MAX_SPLITS : s);
 }
 
 hipError_t launch_paged_attend(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {

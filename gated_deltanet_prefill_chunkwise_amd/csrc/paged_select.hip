@@ -10,8 +10,8 @@
 //
 // score_kernel: 16 rows of A are (token, head) pairs, 16 columns of B pages;
 // tokens of one tile that belong to different requests are taken request by
-// request.  pick_kernel: the K largest of a row by bisection of their bit
-// patterns (counts by ballot), written in rising order.  Bound: latency for a
+// request.  pick_kernel: the K largest of a row by halving the range of
+// their bit patterns (counts by ballot), written in rising order.  Bound: latency for a
 // decode step (the codes of a request are read once: 1/128 of its keys and
 // values at P = 64), the counting for prompts.
 #include "common.h"
@@ -34,17 +34,23 @@ template <typename E> __device__ __forceinline__ void ld16f(const E* p, float (&
 
 constexpr int SW = 4;      // waves of a score workgroup
 
-// Grid: (token tiles, heads, page splits).  GP = 16-row share of a token: G
-// rounded up to a power of two, at most 16 (larger groups in several passes).
-template <typename E, int D>
+// Grid: (groups of token tiles, heads, page splits).  GP: the rows of a tile
+// that a token takes, G rounded up to a power of two, or 16 (larger groups in
+// several passes).  SHARE: the waves take a tile of tokens each and all walk
+// the same pages (rows that mostly belong to one request: prompts); otherwise
+// the waves share a tile and divide the pages (a few rows of many requests).
+// Eight page groups are looked up at a time and requested one ahead.
+template <typename E, int D, bool SHARE>
 __global__ __launch_bounds__(64 * SW) void score_kernel(PageSelectArgs a, int GP) {
   constexpr int NS = D / 64;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, g = lane >> 4;
   const int TT = 16 / GP;                               // tokens of a tile
-  const int row0 = blockIdx.x * TT, h = blockIdx.y;
+  const int row0 = (SHARE ? blockIdx.x * SW + wave : blockIdx.x) * TT, h = blockIdx.y;
   const int MT = (a.G + 15) / 16;
   const int my_row = row0 + n / GP, my_head = n % GP;   // of the A operand
+  const int first = 16 * (SHARE ? blockIdx.z : blockIdx.z * SW + wave);
+  const int step = 16 * (SHARE ? gridDim.z : SW * gridDim.z);
 
   for (int mt = 0; mt < MT; ++mt) {
     // codes of the queries: A operand, lane (n, g) elements 64 s + 16 g ..
@@ -68,6 +74,7 @@ __global__ __launch_bounds__(64 * SW) void score_kernel(PageSelectArgs a, int GP
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const int e = top == 0.f ? 0 : max(ilogbf(top) - 6, -126);
       sq = ldexpf(1.f, e);
+      const float inv = ldexpf(1.f, -e);                // a normal number: e <= 121
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -75,7 +82,7 @@ __global__ __launch_bounds__(64 * SW) void score_kernel(PageSelectArgs a, int GP
           uint32_t u = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float z = fminf(fmaxf(rintf(ldexpf(x[s][4 * w + i], -e)), -127.f), 127.f);
+            const float z = fminf(fmaxf(rintf(x[s][4 * w + i] * inv), -127.f), 127.f);
             u |= ((uint32_t)(int)z & 255u) << (8 * i);
           }
           qc[s][w] = (int)u;
@@ -100,40 +107,58 @@ __global__ __launch_bounds__(64 * SW) void score_kernel(PageSelectArgs a, int GP
       if (len <= 0) continue;
       const int nb = (len + (1 << a.lp) - 1) >> a.lp;
       const int32_t* table = a.table + (size_t)req * a.W;
-      for (int p0 = 16 * (blockIdx.z * SW + wave); p0 < nb; p0 += 16 * SW * gridDim.z) {
-        const int j = p0 + n;
-        const int page = j < nb ? table[j] : -1;
-        const bool ok = page >= 0 && page < a.n_pages;
-        const size_t at = (size_t)(ok ? page : 0) * a.Hkv + h;
-        const int8_t* cp = a.codes + at * D + 16 * g;
-        i32x4 acc = {0, 0, 0, 0};
+      auto put = [&](int j, int t, float x) {
+        if (t < tok || t > last || j >= nb) return;
+        float* to = a.score + ((size_t)(row0 + t) * a.Hkv + h) * a.NB + j;
+        *to = mt == 0 ? x : fmaxf(*to, x);
+      };
+      for (int p0 = first; p0 < nb; p0 += 4 * step) {
+        int page[4];
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(qc[s], *reinterpret_cast<const i32x4*>(cp + 64 * s), acc, 0, 0, 0);
-        const float sk = a.scale[at];
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool head = 16 * mt + (4 * g + i) % GP < a.G;
-          const float x = ((float)acc[i] * sr[i]) * sk;
-          v[i] = ok && head && x == x ? x : -INFINITY;
+        for (int u = 0; u < 4; ++u) {
+          const int j = p0 + u * step + n;
+          page[u] = j < nb ? table[j] : -1;
         }
-        auto put = [&](int t, float x) {
-          if (t < tok || t > last || j >= nb) return;
-          float* to = a.score + ((size_t)(row0 + t) * a.Hkv + h) * a.NB + j;
-          *to = mt == 0 ? x : fmaxf(*to, x);
-        };
-        if (GP == 1) {
+        i32x4 kc[4][NS];
+        float sk[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) put(4 * g + i, v[i]);
-        } else if (GP == 2) {
-          put(2 * g, fmaxf(v[0], v[1]));
-          put(2 * g + 1, fmaxf(v[2], v[3]));
-        } else {
-          float x = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-          if (GP >= 8) x = fmaxf(x, __shfl_xor(x, 16, 64));
-          if (GP == 16) x = fmaxf(x, __shfl_xor(x, 32, 64));
-          if ((4 * g) % GP == 0) put(4 * g / GP, x);
+        for (int u = 0; u < 4; ++u) {
+          const bool ok = page[u] >= 0 && page[u] < a.n_pages;
+          const size_t at = (size_t)(ok ? page[u] : 0) * a.Hkv + h;
+          const int8_t* cp = a.codes + at * D + 16 * g;
+          if (p0 + u * step < nb) {                     // uniform
+#pragma unroll
+            for (int s = 0; s < NS; ++s) kc[u][s] = *reinterpret_cast<const i32x4*>(cp + 64 * s);
+            sk[u] = a.scale[at];
+          }
+          if (!ok) sk[u] = __builtin_nanf("");
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (p0 + u * step >= nb) break;
+          i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(qc[s], kc[u][s], acc, 0, 0, 0);
+          const int j = p0 + u * step + n;
+          float v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool head = 16 * mt + (4 * g + i) % GP < a.G;
+            const float x = ((float)acc[i] * sr[i]) * sk[u];
+            v[i] = head && x == x ? x : -INFINITY;
+          }
+          if (GP == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(j, 4 * g + i, v[i]);
+          } else if (GP == 2) {
+            put(j, 2 * g, fmaxf(v[0], v[1]));
+            put(j, 2 * g + 1, fmaxf(v[2], v[3]));
+          } else {
+            float x = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+            if (GP >= 8) x = fmaxf(x, __shfl_xor(x, 16, 64));
+            if (GP == 16) x = fmaxf(x, __shfl_xor(x, 32, 64));
+            if ((4 * g) % GP == 0) put(j, 4 * g / GP, x);
+          }
         }
       }
     }
@@ -144,7 +169,7 @@ __global__ __launch_bounds__(64 * SW) void score_kernel(PageSelectArgs a, int GP
 template <int NT, int NR>
 __global__ __launch_bounds__(NT) void pick_kernel(PageSelectArgs a) {
   constexpr int NWV = NT / 64;
-  __shared__ int part[2][NWV][2];
+  __shared__ int part[2][NWV][3];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const size_t rh = blockIdx.x;
   const int row = (int)(rh / a.Hkv);
@@ -174,24 +199,31 @@ __global__ __launch_bounds__(NT) void pick_kernel(PageSelectArgs a) {
     }
   }
   int flip = 0;
-  auto total = [&](int x) {                            // sum over the waves of a uniform count
-    if (NWV == 1) return x;
-    if (lane == 0) part[flip][wave][0] = x;
+  auto total = [&](int (&x)[3]) {                      // sums over the waves of uniform counts
+    if (NWV == 1) return;
+    if (lane < 3) part[flip][wave][lane] = lane == 0 ? x[0] : lane == 1 ? x[1] : x[2];
     __syncthreads();
-    int t = 0;
+    x[0] = x[1] = x[2] = 0;
 #pragma unroll
-    for (int w = 0; w < NWV; ++w) t += part[flip][w][0];
+    for (int w = 0; w < NWV; ++w)
+#pragma unroll
+      for (int u = 0; u < 3; ++u) x[u] += part[flip][w][u];
     flip ^= 1;
-    return t;
   };
-  // the largest T with at least `want` keys >= T
+  // A T with `want` keys >= T, or the largest with more; two bits at a time,
+  // as a round of several waves costs a barrier.
   uint32_t T = 0u;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t t = T | (1u << bit);
-    int cnt = 0;
+  bool exact = false;
+  for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
+    int c[3] = {0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < NR; ++i) cnt += __builtin_popcountll(__ballot(key[i] >= t));
-    if (total(cnt) >= want) T = t;
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int u = 0; u < 3; ++u) c[u] += __builtin_popcountll(__ballot(key[i] >= (T | ((uint32_t)(u + 1) << bit))));
+    total(c);
+    const int u = c[2] >= want ? 3 : c[1] >= want ? 2 : c[0] >= want ? 1 : 0;
+    T |= (uint32_t)u << bit;
+    exact = u > 0 && c[u - 1] == want;
   }
   int above = 0, equal = 0;
 #pragma unroll
@@ -226,19 +258,29 @@ __global__ __launch_bounds__(NT) void pick_kernel(PageSelectArgs a) {
   }
 }
 
-template <typename E> hipError_t launch_score(const PageSelectArgs& a, int d, hipStream_t s) {
-  int gp = 1;
-  while (gp < a.G && gp < 16) gp <<= 1;
-  const int tiles = (a.R + 16 / gp - 1) / (16 / gp);
-  // enough workgroups for the chip, but 64 pages at least for each
-  const long long base = (long long)tiles * a.Hkv;
-  const int most = (a.NB + 16 * SW - 1) / (16 * SW);
-  const int z = (int)(base >= 1024 ? 1 : (1024 / base < most ? 1024 / base : most));
-  const dim3 grid(tiles, a.Hkv, z < 1 ? 1 : z);
-  if (d == 64) hipLaunchKernelGGL((score_kernel<E, 64>), grid, dim3(64 * SW), 0, s, a, gp);
-  else if (d == 128) hipLaunchKernelGGL((score_kernel<E, 128>), grid, dim3(64 * SW), 0, s, a, gp);
-  else hipLaunchKernelGGL((score_kernel<E, 256>), grid, dim3(64 * SW), 0, s, a, gp);
+template <typename E, bool SHARE>
+hipError_t launch_score_s(const PageSelectArgs& a, int d, int gp, dim3 grid, hipStream_t s) {
+  if (d == 64) hipLaunchKernelGGL((score_kernel<E, 64, SHARE>), grid, dim3(64 * SW), 0, s, a, gp);
+  else if (d == 128) hipLaunchKernelGGL((score_kernel<E, 128, SHARE>), grid, dim3(64 * SW), 0, s, a, gp);
+  else hipLaunchKernelGGL((score_kernel<E, 256, SHARE>), grid, dim3(64 * SW), 0, s, a, gp);
   return hipGetLastError();
+}
+
+template <typename E> hipError_t launch_score(const PageSelectArgs& a, int d, hipStream_t s) {
+  // Rows that share requests (more rows than requests) fill a tile; a row of
+  // its own request takes one alone, so that no wave walks several tables.
+  const bool share = a.R > a.B;
+  int gp = 16;
+  if (share)
+    for (gp = 1; gp < a.G && gp < 16;) gp <<= 1;
+  const int tt = 16 / gp;
+  const long long tiles = ((long long)a.R + tt - 1) / tt;
+  const long long gx = share ? (tiles + SW - 1) / SW : tiles;
+  // page splits: enough workgroups for the chip, each wave its four page groups
+  const int run = share ? 64 : 64 * SW;
+  const long long most = (a.NB + run - 1) / run, want = (2048 + gx * a.Hkv - 1) / (gx * a.Hkv);
+  const dim3 grid((unsigned)gx, a.Hkv, (unsigned)(want < most ? want : most));
+  return share ? launch_score_s<E, true>(a, d, gp, grid, s) : launch_score_s<E, false>(a, d, gp, grid, s);
 }
 
 }  // namespace
@@ -252,7 +294,7 @@ hipError_t launch_paged_select(const PageSelectArgs& a, int dtype, int d, hipStr
   if (a.NB <= 64) hipLaunchKernelGGL((pick_kernel<64, 1>), grid, dim3(64), 0, s, a);
   else if (a.NB <= 256) hipLaunchKernelGGL((pick_kernel<64, 4>), grid, dim3(64), 0, s, a);
   else if (a.NB <= 1024) hipLaunchKernelGGL((pick_kernel<256, 4>), grid, dim3(256), 0, s, a);
-  else if (a.NB <= 4096) hipLaunchKernelGGL((pick_kernel<1024, 4>), grid, dim3(1024), 0, s, a);
+  else if (a.NB <= 4096) hipLaunchKernelGGL((pick_kernel<256, 16>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((pick_kernel<1024, 16>), grid, dim3(1024), 0, s, a);
   return hipGetLastError();
 }
