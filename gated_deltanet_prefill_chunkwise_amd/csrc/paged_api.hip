@@ -10,6 +10,7 @@ namespace {
 
 using namespace sgdn;
 
+constexpr size_t NO_WORKSPACE = 256;   // answer of sgdn_paged_workspace_bytes where none is used
 constexpr int MAX_LIST = 4096;     // blocks of a list
 constexpr int MAX_NB = 16384;      // blocks of a row that are ranked
 
@@ -75,14 +76,14 @@ AttendPlan attend_plan(const sgdn_paged* p, int n_blocks) {
     pl.off_ml = align256(parts * p->d * sizeof(float));
     pl.total = pl.off_ml + align256(parts * 2 * sizeof(float));
   }
-  if (pl.total == 0) pl.total = 256;
+  if (pl.total == 0) pl.total = NO_WORKSPACE;
   return pl;
 }
 
 size_t select_bytes(const sgdn_paged* p, int n_blocks) {
   const int nb = (longest(p) + p->page - 1) / p->page;
-  if (nb <= n_blocks || p->rows == 0) return 256;
-  return align256((size_t)p->rows * p->n_kv * nb * sizeof(float));
+  if (nb <= n_blocks || p->rows == 0) return NO_WORKSPACE;
+  return NO_WORKSPACE + align256((size_t)p->rows * p->n_kv * nb * sizeof(float));
 }
 
 int attend(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache, const void* v_cache,
@@ -94,13 +95,14 @@ int attend(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache,
   if (p->o_dtype != SGDN_F32 && p->o_dtype != SGDN_BF16 && p->o_dtype != SGDN_F16) return SGDN_EINVAL;
   if (!isfinite(scale)) return SGDN_EINVAL;
   if (p->rows == 0) return SGDN_OK;
-  if (!q || !k_cache || !v_cache || !table || !row_len || !o || !ws) return SGDN_EINVAL;
+  if (!q || !k_cache || !v_cache || !table || !row_len || !o) return SGDN_EINVAL;
   if (row_req == nullptr && p->rows > p->batch) return SGDN_EINVAL;
   if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(o) || misaligned(ws))
     return SGDN_EINVAL;
   if (bad_stride(ldq, (int64_t)p->n_q * p->d, p->dtype)) return SGDN_EINVAL;
   const AttendPlan pl = attend_plan(p, n_blocks);
-  if (ws_bytes < pl.total) return SGDN_EWORKSPACE;
+  if (pl.total > NO_WORKSPACE && !ws) return SGDN_EINVAL;
+  if (pl.total > NO_WORKSPACE && ws_bytes < pl.total) return SGDN_EWORKSPACE;
   PageAttendArgs a;
   a.q = q; a.ldq = ldq; a.kc = k_cache; a.vc = v_cache;
   a.table = table; a.row_req = row_req; a.row_len = row_len; a.blocks = blocks;
@@ -203,11 +205,13 @@ int sgdn_paged_select(const sgdn_paged* p, const void* q, int64_t ldq, const int
   const int nb = (longest(p) + p->page - 1) / p->page;
   if (nb > MAX_NB) return SGDN_EUNSUPPORTED;
   if (p->rows == 0) return SGDN_OK;
-  if (!q || !codes || !scale || !table || !row_len || !blocks || !ws) return SGDN_EINVAL;
+  if (!q || !codes || !scale || !table || !row_len || !blocks) return SGDN_EINVAL;
   if (row_req == nullptr && p->rows > p->batch) return SGDN_EINVAL;
   if (misaligned(q) || misaligned(codes) || misaligned(ws)) return SGDN_EINVAL;
   if (bad_stride(ldq, (int64_t)p->n_q * p->d, p->dtype)) return SGDN_EINVAL;
-  if (ws_bytes < select_bytes(p, n_blocks)) return SGDN_EWORKSPACE;
+  const size_t need = select_bytes(p, n_blocks);
+  if (need > NO_WORKSPACE && !ws) return SGDN_EINVAL;
+  if (need > NO_WORKSPACE && ws_bytes < need) return SGDN_EWORKSPACE;
   const PageSelectArgs a{q, ldq, codes, scale, table, row_req, row_len, blocks, static_cast<float*>(ws),
                          p->rows, p->batch, p->n_q, p->n_kv, p->n_q / p->n_kv,
                          log2_page(p->page), p->n_pages, p->width, longest(p), nb,

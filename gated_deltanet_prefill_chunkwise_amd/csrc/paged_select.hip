@@ -8,12 +8,13 @@
 // exact as fp32 and under both powers of two; hence every evaluation order
 // gives the same score and the choice has no border cases.
 //
-// score_kernel: 16 rows of A are (token, head) pairs, 16 columns of B pages;
-// tokens of one tile that belong to different requests are taken request by
-// request.  pick_kernel: the K largest of a row by halving the range of
+// score_*_kernel: 16 rows of A are (token, head) pairs, 16 columns of B pages.
+// pick_kernel: the K largest of a row by halving the range of
 // their bit patterns (counts by ballot), written in rising order.  Bound: latency for a
 // decode step (the codes of a request are read once: 1/128 of its keys and
 // values at P = 64), the counting for prompts.
+#include <type_traits>
+
 #include "common.h"
 #include "paged.h"
 
@@ -23,264 +24,486 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// 16 neighbouring elements as fp32.
-template <typename E> __device__ __forceinline__ void ld16f(const E* p, float (&x)[16]) {
-  union { V16 w[sizeof(E)]; E e[16]; } f;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(E); ++i) f.w[i] = ldv(p + i * (16 / (int)sizeof(E)));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = to_f(f.e[i]);
-}
-
 constexpr int SW = 4;      // waves of a score workgroup
 
-// Grid: (groups of token tiles, heads, page splits).  GP: the rows of a tile
-// that a token takes, G rounded up to a power of two, or 16 (larger groups in
-// several passes).  SHARE: the waves take a tile of tokens each and all walk
-// the same pages (rows that mostly belong to one request: prompts); otherwise
-// the waves share a tile and divide the pages (a few rows of many requests).
-// Eight page groups are looked up at a time and requested one ahead.
-template <typename E, int D, bool SHARE>
-__global__ __launch_bounds__(64 * SW) void score_kernel(PageSelectArgs a, int GP) {
-  constexpr int NS = D / 64;
+// Maximum of two numbers (no NaN here): fmaxf would first quiet both.
+__device__ __forceinline__ float max2(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+
+// Maximum over lanes l and l ^ 16, l and l ^ 32.
+__device__ __forceinline__ float max_x16(float x) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t p = r[0], q = r[1];
+  return max2(__builtin_bit_cast(float, p), __builtin_bit_cast(float, q));
+}
+__device__ __forceinline__ float max_x32(float x) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t p = r[0], q = r[1];
+  return max2(__builtin_bit_cast(float, p), __builtin_bit_cast(float, q));
+}
+
+// A query tile as the A operand: lane (n, g) elements 64 s + 16 g .. + 15 of
+// row n, as codes; sr: the powers of two of D's rows 4g + j.
+template <typename E, int NS> struct Query {
+  i32x4 c[NS];
+  float sr[4];
+};
+// Raw elements of a lane.  (Loads here take a place that can be read where
+// they have none of their own: under a condition each would wait for itself.)
+template <typename E, int NS> struct RawQ {
+  V16 w[NS][sizeof(E)];
+  __device__ __forceinline__ void load(const E* q) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(E); ++i) w[s][i] = ldv(q + 64 * s + i * (16 / (int)sizeof(E)));
+  }
+  __device__ __forceinline__ float at(int s, int i) const {
+    constexpr int PER = 16 / (int)sizeof(E);
+    const uint32_t x = w[s][i / PER].w[(i % PER) * (int)sizeof(E) / 4];
+    if constexpr (sizeof(E) == 4) {
+      return __builtin_bit_cast(float, x);
+    } else {
+      const uint16_t half = (uint16_t)((i & 1) ? x >> 16 : x);
+      return to_f(__builtin_bit_cast(E, half));
+    }
+  }
+};
+// Codes as the low byte of x 2^-e + 1.5 2^23, whose last place is 1: the sum
+// rounds to the nearest whole number, ties to even, in two's complement.
+template <typename E, int NS> __device__ __forceinline__ void quantise(const RawQ<E, NS>& raw, int g, Query<E, NS>& q) {
+  uint32_t top = 0u;                                    // |x| by its bits: NaN over infinity over numbers
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __builtin_bit_cast(uint32_t, raw.at(s, i)) & 0x7fffffffu);
+  const bool odd = __ballot(top >= 0x7f800000u) != 0ull;   // uniform: some element counts as 0
+  if (odd) {
+    top = 0u;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, raw.at(s, i)) & 0x7fffffffu;
+        if (u < 0x7f800000u) top = max(top, u);
+      }
+  }
+  const float t = max_x32(max_x16(__builtin_bit_cast(float, top)));
+  const int e = t == 0.f ? 0 : max(ilogbf(t) - 6, -126);
+  const float inv = ldexpf(1.f, -e), sq = ldexpf(1.f, e);   // normal numbers: -126 <= e <= 121
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = raw.at(s, 4 * w + i);
+        if (odd && (__builtin_bit_cast(uint32_t, x) & 0x7fffffffu) >= 0x7f800000u) x = 0.f;
+        z[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(x * inv, -127.f, 127.f) + 12582912.f);
+      }
+      const uint32_t lo = __builtin_amdgcn_perm(z[1], z[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(z[3], z[2], 0x04000c0cu);
+      q.c[s][w] = (int)(lo | hi);
+    }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q.sr[j] = __shfl(sq, 4 * g + j, 64);
+}
+
+// Summaries of 16 pages as the B operand: lane (n, g) bytes 64 s + 16 g .. of
+// page n.  A page that is none has the scale NaN, which no maximum takes.
+template <int NS> struct Pages {
+  i32x4 c[NS];
+  float sk;
+};
+template <int NS> __device__ __forceinline__ void load_pages(const PageSelectArgs& a, int page, int h, int g, Pages<NS>& p) {
+  const bool ok = page >= 0 && page < a.n_pages;
+  const size_t at = (size_t)(ok ? page : 0) * a.Hkv + h;
+  const int8_t* cp = a.codes + at * (64 * NS) + 16 * g;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) p.c[s] = *reinterpret_cast<const i32x4*>(cp + 64 * s);
+  p.sk = a.scale[at];
+  if (!ok) p.sk = __builtin_nanf("");
+}
+
+// The products of a tile: v[j] = (q8 . codes) sq for row 4g + j and page n.
+// The page's scale is positive, so the maximum over heads may come before it.
+template <typename E, int NS> __device__ __forceinline__ void products(const Query<E, NS>& q, const Pages<NS>& p, float (&v)[4]) {
+  i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < NS; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(q.c[s], p.c[s], acc, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * q.sr[j];
+}
+__device__ __forceinline__ float scaled(float x, float sk) {
+  const float y = x * sk;
+  return y == y ? y : -INFINITY;
+}
+
+// Rows of a request each (decode): the waves of a workgroup take HS heads,
+// whose codes of a page are neighbours, and divide the row's pages by what is
+// left.  A workgroup takes one of Z shares of the pages; the shares of all
+// heads follow each other on one XCD (workgroup id mod 8), which then reads a
+// page's scales once.  A wave has a batch of four page groups on its way and
+// looks up the next, the first before it turns to its query, as nearly all of
+// its time is waiting.
+template <typename E, int D>
+__global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, int HS, int Z) {
+  constexpr int NS = D / 64, PG = 4;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, g = lane >> 4;
-  const int TT = 16 / GP;                               // tokens of a tile
-  const int row0 = (SHARE ? blockIdx.x * SW + wave : blockIdx.x) * TT, h = blockIdx.y;
-  const int MT = (a.G + 15) / 16;
-  const int my_row = row0 + n / GP, my_head = n % GP;   // of the A operand
-  const int first = 16 * (SHARE ? blockIdx.z : blockIdx.z * SW + wave);
-  const int step = 16 * (SHARE ? gridDim.z : SW * gridDim.z);
-
-  for (int mt = 0; mt < MT; ++mt) {
-    // codes of the queries: A operand, lane (n, g) elements 64 s + 16 g ..
-    i32x4 qc[NS];
-    float sq;
-    {
-      const int hd = 16 * mt + my_head;
-      const bool real = my_row < a.R && hd < a.G;
-      const E* q = static_cast<const E*>(a.q) + (real ? my_row * a.ldq + (size_t)(h * a.G + hd) * D : 0) + 16 * g;
-      float x[NS][16], top = 0.f;
+  const int HB = (a.Hkv + HS - 1) / HS, PS = SW / HS;
+  const int k = blockIdx.x >> 3, unit = (k / HB) * 8 + (blockIdx.x & 7);
+  const int r = unit / Z, share = unit - r * Z;
+  const int h = (k % HB) * HS + wave % HS;
+  if (r >= a.R || h >= a.Hkv) return;
+  const int req = a.row_req == nullptr ? r : a.row_req[r];
+  const int len = min(a.row_len[r], a.max_len);
+  if (req < 0 || req >= a.B || len <= 0) return;
+  const int nb = (len + (1 << a.lp) - 1) >> a.lp;
+  const int32_t* table = a.table + (size_t)req * a.W;
+  float* to = a.score + ((size_t)r * a.Hkv + h) * a.NB;
+  const int step = 16 * PG * PS * Z, first = 16 * PG * (share * PS + wave / HS);
+  if (first >= nb) return;
+  for (int h0 = 0; h0 < a.G; h0 += 16) {
+    RawQ<E, NS> raw;                                     // heads beyond the group: the last one again
+    raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + min(h0 + n, a.G - 1)) * D + 16 * g);
+    int page[PG];
+    auto look_up = [&](int p0) {
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        ld16f(q + 64 * s, x[s]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (!real || !__builtin_isfinite(x[s][i])) x[s][i] = 0.f;
-          top = fmaxf(top, fabsf(x[s][i]));
-        }
+      for (int u = 0; u < PG; ++u) {
+        const int j = p0 + 16 * u + n;
+        page[u] = table[min(j, nb - 1)];
       }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const int e = top == 0.f ? 0 : max(ilogbf(top) - 6, -126);
-      sq = ldexpf(1.f, e);
-      const float inv = ldexpf(1.f, -e);                // a normal number: e <= 121
+    };
+    Pages<NS> pg[PG];
+    look_up(first);
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
+    for (int u = 0; u < PG; ++u) load_pages<NS>(a, page[u], h, g, pg[u]);
+    look_up(first + step);
+    Query<E, NS> q;
+    quantise<E, NS>(raw, g, q);
+    for (int p0 = first; p0 < nb; p0 += step) {
+      float x[PG], sk[PG];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t u = 0;
+      for (int u = 0; u < PG; ++u) {
+        float v[4];
+        products<E, NS>(q, pg[u], v);
+        x[u] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float z = fminf(fmaxf(rintf(x[s][4 * w + i] * inv), -127.f), 127.f);
-            u |= ((uint32_t)(int)z & 255u) << (8 * i);
-          }
-          qc[s][w] = (int)u;
-        }
+        for (int j = 0; j < 4; ++j) x[u] = max2(x[u], v[j]);
+        sk[u] = pg[u].sk;
+      }
+      if (p0 + step < nb) {
+#pragma unroll
+        for (int u = 0; u < PG; ++u) load_pages<NS>(a, page[u], h, g, pg[u]);
+        look_up(p0 + 2 * step);
+      }
+#pragma unroll
+      for (int u = 0; u < PG; ++u) {
+        const float y = scaled(max_x32(max_x16(x[u])), sk[u]);
+        const int j = p0 + 16 * u + n;
+        if (g == 0 && j < nb) to[j] = h0 == 0 ? y : fmaxf(to[j], y);   // written by this lane
+      }
     }
-    float sr[4];                                        // sq of D's rows 4g + j
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sr[j] = __shfl(sq, 4 * g + j, 64);
+  }
+}
 
-    for (int tok = 0; tok < TT; ++tok) {                // uniform
-      const int r = row0 + tok;
-      if (r >= a.R) break;
-      const int req = a.row_req == nullptr ? r : a.row_req[r];
-      if (req < 0 || req >= a.B) continue;
-      if (tok > 0 && a.row_req != nullptr && a.row_req[r - 1] == req) continue;   // taken with the token before
-      // the run of tokens of this request in the tile, and the longest of them
-      int last = tok, len = min(a.row_len[r], a.max_len);
-      while (last + 1 < TT && row0 + last + 1 < a.R && a.row_req != nullptr && a.row_req[row0 + last + 1] == req) {
-        ++last;
-        len = max(len, min(a.row_len[row0 + last], a.max_len));
+// Many rows of a request (prompts), G <= 16: a tile holds 16 / GP tokens (GP: G
+// rounded up to a power of two), a wave QT tiles, which all use the pages that
+// it loads.  Tokens of different requests in a wave are taken request by
+// request.
+constexpr int tiles_of_wave(int gp) { return gp == 1 ? 2 : 4; }   // QT (a lane's addresses fill the registers at GP 1)
+template <typename E, int D, int GP>
+__global__ __launch_bounds__(64 * SW, D == 256 ? 2 : 3) void score_rows_kernel(PageSelectArgs a) {
+  constexpr int NS = D / 64, QT = tiles_of_wave(GP), TT = 16 / GP, TW = QT * TT;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int n = lane & 15, g = lane >> 4;
+  const int row0 = (blockIdx.x * SW + wave) * TW, h = blockIdx.y;
+  if (row0 >= a.R) return;
+  Query<E, NS> q[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int r = min(row0 + t * TT + n / GP, a.R - 1), hd = min(n % GP, a.G - 1);
+    RawQ<E, NS> raw;                                     // rows and heads beyond the last: the last again
+    raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + hd) * D + 16 * g);
+    quantise<E, NS>(raw, g, q[t]);
+  }
+  // lane l: request and length of the wave's token l
+  int req = -1, len = 0;
+  if (lane < TW && row0 + lane < a.R) {
+    req = a.row_req[row0 + lane];
+    len = min(a.row_len[row0 + lane], a.max_len);
+    if (req < 0 || req >= a.B || len <= 0) req = -1;
+  }
+  uint64_t todo = __ballot(req >= 0);
+  while (todo != 0) {
+    const int now = __builtin_amdgcn_readlane(req, __builtin_ctzll(todo));
+    const uint64_t mine = __ballot(req == now) & todo;
+    todo &= ~mine;
+    int most = req == now ? len : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) most = max(most, __shfl_xor(most, o, 64));
+    const int nb = __builtin_amdgcn_readfirstlane((most + (1 << a.lp) - 1) >> a.lp);
+    const int32_t* table = a.table + (size_t)now * a.W;
+    const int step = 32 * gridDim.z, first = 32 * blockIdx.z;
+    if (first >= nb) continue;
+    // where this lane's scores go, by tile, and whether they are of this request
+    constexpr int PER = GP >= 4 ? 1 : 4 / GP;            // tokens of a lane's four rows
+    float* to[QT][PER];
+    bool ours[QT][PER];
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int tok = t * TT + 4 * g / GP + i;
+        ours[t][i] = (4 * g) % GP == 0 || GP < 4 ? ((mine >> tok) & 1) != 0 : false;
+        to[t][i] = a.score + ((size_t)(row0 + tok) * a.Hkv + h) * a.NB + n;
       }
-      if (len <= 0) continue;
-      const int nb = (len + (1 << a.lp) - 1) >> a.lp;
-      const int32_t* table = a.table + (size_t)req * a.W;
-      auto put = [&](int j, int t, float x) {
-        if (t < tok || t > last || j >= nb) return;
-        float* to = a.score + ((size_t)(row0 + t) * a.Hkv + h) * a.NB + j;
-        *to = mt == 0 ? x : fmaxf(*to, x);
-      };
-      for (int p0 = first; p0 < nb; p0 += 4 * step) {
-        int page[4];
+    // two groups at a time; the next two, and the page numbers behind, on their way
+    Pages<NS> next[2];
+    int page[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int j = p0 + u * step + n;
-          page[u] = j < nb ? table[j] : -1;
-        }
-        i32x4 kc[4][NS];
-        float sk[4];
+    for (int u = 0; u < 2; ++u) load_pages<NS>(a, table[min(first + 16 * u + n, nb - 1)], h, g, next[u]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool ok = page[u] >= 0 && page[u] < a.n_pages;
-          const size_t at = (size_t)(ok ? page[u] : 0) * a.Hkv + h;
-          const int8_t* cp = a.codes + at * D + 16 * g;
-          if (p0 + u * step < nb) {                     // uniform
+    for (int u = 0; u < 2; ++u) page[u] = table[min(first + step + 16 * u + n, nb - 1)];
+    for (int p0 = first; p0 < nb; p0 += step) {
+      const Pages<NS> pg[2] = {next[0], next[1]};
+      if (p0 + step < nb) {
 #pragma unroll
-            for (int s = 0; s < NS; ++s) kc[u][s] = *reinterpret_cast<const i32x4*>(cp + 64 * s);
-            sk[u] = a.scale[at];
-          }
-          if (!ok) sk[u] = __builtin_nanf("");
-        }
+        for (int u = 0; u < 2; ++u) load_pages<NS>(a, page[u], h, g, next[u]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (p0 + u * step >= nb) break;
-          i32x4 acc = {0, 0, 0, 0};
+        for (int u = 0; u < 2; ++u) page[u] = table[min(p0 + 2 * step + 16 * u + n, nb - 1)];
+      }
 #pragma unroll
-          for (int s = 0; s < NS; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(qc[s], kc[u][s], acc, 0, 0, 0);
-          const int j = p0 + u * step + n;
+      for (int u = 0; u < 2; ++u) {
+        const bool in = p0 + 16 * u + n < nb;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
           float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool head = 16 * mt + (4 * g + i) % GP < a.G;
-            const float x = ((float)acc[i] * sr[i]) * sk[u];
-            v[i] = head && x == x ? x : -INFINITY;
-          }
-          if (GP == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) put(j, 4 * g + i, v[i]);
-          } else if (GP == 2) {
-            put(j, 2 * g, fmaxf(v[0], v[1]));
-            put(j, 2 * g + 1, fmaxf(v[2], v[3]));
+          products<E, NS>(q[t], pg[u], v);
+          float x[PER];
+          if constexpr (GP >= 4) {
+            x[0] = max2(max2(v[0], v[1]), max2(v[2], v[3]));
+            if (GP >= 8) x[0] = max_x16(x[0]);
+            if (GP == 16) x[0] = max_x32(x[0]);
+          } else if constexpr (GP == 2) {
+            x[0] = max2(v[0], v[1]);
+            x[1] = max2(v[2], v[3]);
           } else {
-            float x = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-            if (GP >= 8) x = fmaxf(x, __shfl_xor(x, 16, 64));
-            if (GP == 16) x = fmaxf(x, __shfl_xor(x, 32, 64));
-            if ((4 * g) % GP == 0) put(j, 4 * g / GP, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = v[i];
           }
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            if (in && ours[t][i]) to[t][i][p0 + 16 * u] = scaled(x[i], pg[u].sk);
         }
       }
     }
   }
 }
 
-// One workgroup of NT threads per (row, head), up to NR scores per thread.
-template <int NT, int NR>
-__global__ __launch_bounds__(NT) void pick_kernel(PageSelectArgs a) {
-  constexpr int NWV = NT / 64;
-  __shared__ int part[2][NWV][3];
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const size_t rh = blockIdx.x;
+// Orders a wave's own LDS writes before its reads.
+__device__ __forceinline__ void lds_wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// Maximum over a wave's lanes (all active) by row shifts and broadcasts.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  auto step = [&](auto ctrl) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  step(std::integral_constant<int, 0x111>{});         // row_shr 1, 2, 4, 8
+  step(std::integral_constant<int, 0x112>{});
+  step(std::integral_constant<int, 0x114>{});
+  step(std::integral_constant<int, 0x118>{});
+  step(std::integral_constant<int, 0x142>{});         // row_bcast 15, 31
+  step(std::integral_constant<int, 0x143>{});
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// NWV waves per (row, head), up to NR scores per lane; single waves come four
+// to a workgroup.
+template <int NWV, int NR>
+__global__ __launch_bounds__(NWV == 1 ? 256 : 64 * NWV) void pick_kernel(PageSelectArgs a) {
+  constexpr int NT = 64 * NWV;
+  constexpr int ROWS = NWV == 1 ? 4 : 1;
+  // Candidates that are ranked one against all: a step of the ranking costs a
+  // wave about what NR / 4 + 4 steps of narrowing do, without their barriers.
+  constexpr int FEW = NWV == 1 ? 8 : 16;
+  __shared__ uint32_t part[2][NWV][2];
+  __shared__ uint32_t cands[ROWS][64];
+  const int lane = lane_id(), w0 = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = NWV == 1 ? 0 : w0, tid = NWV == 1 ? lane : (int)threadIdx.x;
+  uint32_t* cand = cands[NWV == 1 ? w0 : 0];
+  const int64_t rh = (int64_t)blockIdx.x * ROWS + (NWV == 1 ? w0 : 0);
   const int row = (int)(rh / a.Hkv);
+  if (row >= a.R) return;
   const int req = a.row_req == nullptr ? row : a.row_req[row];
   int len = min(a.row_len[row], a.max_len);
   if (req < 0 || req >= a.B) len = 0;
   const int nb = len <= 0 ? 0 : (len + (1 << a.lp) - 1) >> a.lp;
   int32_t* out = a.blocks + rh * a.K;
   const int want = min(a.K, nb);
-  for (int i = want + threadIdx.x; i < a.K; i += NT) out[i] = -1;
+  for (int i = want + tid; i < a.K; i += NT) out[i] = -1;
   if (nb <= a.K) {
-    for (int i = threadIdx.x; i < nb; i += NT) out[i] = i;
+    for (int i = tid; i < nb; i += NT) out[i] = i;
     return;
   }
   // Scores as whole numbers of the same order; wave w holds a run of 64 NR.
   const float* score = a.score + rh * a.NB;
   const int base = wave * 64 * NR;
   uint32_t key[NR];
+  float raw[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) raw[i] = score[min(base + 64 * i + lane, nb - 1)];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int j = base + 64 * i + lane;
-    key[i] = 0u;                                       // beyond the row: under every score
-    if (j < nb) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, score[j] + 0.f);   // -0 counts as 0
-      key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-      if (j < a.n_sink || j >= nb - a.n_local) key[i] = 0xffffffffu;
-    }
+    const uint32_t u = __builtin_bit_cast(uint32_t, raw[i] + 0.f);       // -0 counts as 0
+    key[i] = (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    if (j < a.n_sink || j >= nb - a.n_local) key[i] = 0xffffffffu;
+    if (j >= nb) key[i] = 0u;                            // beyond the row: under every score
   }
   int flip = 0;
-  auto total = [&](int (&x)[3]) {                      // sums over the waves of uniform counts
-    if (NWV == 1) return;
-    if (lane < 3) part[flip][wave][lane] = lane == 0 ? x[0] : lane == 1 ? x[1] : x[2];
+  auto share = [&](uint32_t x, uint32_t y) {             // two uniform numbers of each wave, for all to read
+    if (lane == 0) { part[flip][wave][0] = x; part[flip][wave][1] = y; }
     __syncthreads();
-    x[0] = x[1] = x[2] = 0;
-#pragma unroll
-    for (int w = 0; w < NWV; ++w)
-#pragma unroll
-      for (int u = 0; u < 3; ++u) x[u] += part[flip][w][u];
-    flip ^= 1;
+    flip ^= 1;                                           // the other buffer is free: all have passed it
   };
-  // A T with `want` keys >= T, or the largest with more; two bits at a time,
-  // as a round of several waves costs a barrier.
-  uint32_t T = 0u;
-  bool exact = false;
-  for (int bit = 30; bit >= 0 && !exact; bit -= 2) {
-    int c[3] = {0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int u = 0; u < 3; ++u) c[u] += __builtin_popcountll(__ballot(key[i] >= (T | ((uint32_t)(u + 1) << bit))));
-    total(c);
-    const int u = c[2] >= want ? 3 : c[1] >= want ? 2 : c[0] >= want ? 1 : 0;
-    T |= (uint32_t)u << bit;
-    exact = u > 0 && c[u - 1] == want;
-  }
-  int above = 0, equal = 0;
+  uint32_t top = 0u, low = 0u;
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    above += __builtin_popcountll(__ballot(key[i] > T));
-    equal += __builtin_popcountll(__ballot(key[i] == T));
+    if (key[i] != 0xffffffffu) top = max(top, key[i]);
+    if (key[i] != 0u) low = max(low, ~key[i]);
   }
-  int above0 = 0, equal0 = 0, all_above = above;
+  top = wave_max(top);
+  low = wave_max(low);
   if (NWV > 1) {
-    if (lane == 0) { part[flip][wave][0] = above; part[flip][wave][1] = equal; }
-    __syncthreads();
-    all_above = 0;
+    share(top, low);
 #pragma unroll
     for (int w = 0; w < NWV; ++w) {
-      if (w == wave) above0 = all_above;
-      all_above += part[flip][w][0];
-      if (w < wave) equal0 += part[flip][w][1];
+      top = max(top, part[flip ^ 1][w][0]);
+      low = max(low, part[flip ^ 1][w][1]);
     }
   }
-  const int ties = want - all_above;                   // of the equal ones, the first
-  const uint64_t below = (1ull << lane) - 1ull;
-  int done_a = above0, done_e = equal0;
+  // Narrow lo < hi, clo = count(key >= lo) > want > chi = count(key >= hi), in
+  // turn where the two counts put the wanted rank and in the middle, until at
+  // most FEW keys lie between (or more, all equal).
+  const int forced = a.n_sink + a.n_local;               // nb > K >= forced: the two runs do not meet
+  uint32_t lo = ~low, hi = top + 1;                      // scores stay under 0xff800001
+  int clo = nb, chi = forced;
+  bool even = true;
+  while (clo - chi > FEW && clo != want && chi != want && lo + 1 < hi) {
+    uint32_t mid = lo + ((hi - lo) >> 1);
+    if (even) {
+      const float f = (float)(clo - want) * __builtin_amdgcn_rcpf((float)(clo - chi));
+      mid = lo + (uint32_t)((float)(hi - lo) * f);
+      mid = min(max(mid, lo + 1), hi - 1);
+    }
+    even = !even;
+    int cnt = 0;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) cnt += __builtin_popcountll(__ballot(key[i] >= mid));
+    if (NWV > 1) {
+      share((uint32_t)cnt, 0u);
+      cnt = 0;
+#pragma unroll
+      for (int w = 0; w < NWV; ++w) cnt += (int)part[flip ^ 1][w][0];
+    }
+    if (cnt >= want) { lo = mid; clo = cnt; } else { hi = mid; chi = cnt; }
+  }
+  // Everything >= hi is picked, and want - chi of the m = clo - chi candidates
+  // in lo .. hi - 1: rank them, the first of equal ones in front.
+  const int m = clo - chi, need = want - chi;
+  int above = 0, between = 0;                            // of this wave
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    const bool is_a = key[i] > T, is_e = key[i] == T;
-    const uint64_t ba = __ballot(is_a), be = __ballot(is_e);
-    const int ra = done_a + __builtin_popcountll(ba & below);
-    const int re = done_e + __builtin_popcountll(be & below);
-    if (is_a || (is_e && re < ties)) out[ra + min(re, ties)] = base + 64 * i + lane;
-    done_a += __builtin_popcountll(ba);
-    done_e += __builtin_popcountll(be);
+    above += __builtin_popcountll(__ballot(key[i] >= hi));
+    between += __builtin_popcountll(__ballot(key[i] >= lo && key[i] < hi));
+  }
+  int above0 = 0, between0 = 0;
+  if (NWV > 1) {
+    share((uint32_t)above, (uint32_t)between);
+#pragma unroll
+    for (int w = 0; w < NWV; ++w)
+      if (w < wave) { above0 += (int)part[flip ^ 1][w][0]; between0 += (int)part[flip ^ 1][w][1]; }
+  }
+  const uint64_t below = (1ull << lane) - 1ull;
+  uint64_t picked = ~0ull;                               // by a candidate's place, where m <= 64
+  if (need > 0 && m <= 64) {
+    int c = between0;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const bool is = key[i] >= lo && key[i] < hi;
+      const uint64_t b = __ballot(is);
+      if (b == 0ull) continue;
+      if (is) cand[c + __builtin_popcountll(b & below)] = key[i];
+      c += __builtin_popcountll(b);
+    }
+    if (NWV > 1) __syncthreads(); else lds_wave_fence();
+    const uint32_t mine = lane < m ? cand[lane] : 0u;
+    int rank = 0;
+    for (int j = 0; j < m; ++j) {
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, j);
+      rank += other > mine || (other == mine && j < lane) ? 1 : 0;
+    }
+    picked = __ballot(lane < m && rank < need);
+  }
+  const bool by_place = m > 64;                          // all candidates are equal
+  int done = above0, seen = between0;                    // picked so far, candidates so far
+  if (by_place) done += min(between0, need);
+  else if (need > 0) done += __builtin_popcountll(between0 >= 64 ? picked : picked & ((1ull << between0) - 1ull));
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const bool is = key[i] >= lo && key[i] < hi;
+    const uint64_t ca = __ballot(is), ge = __ballot(key[i] >= hi);
+    if ((ca | ge) == 0ull) continue;
+    const int c = seen + __builtin_popcountll(ca & below);
+    const bool take = key[i] >= hi || (is && need > 0 && (by_place ? c < need : (picked >> c) & 1));
+    const uint64_t b = __ballot(take);
+    if (take) out[done + __builtin_popcountll(b & below)] = base + 64 * i + lane;
+    done += __builtin_popcountll(b);
+    seen += __builtin_popcountll(ca);
   }
 }
 
-template <typename E, bool SHARE>
-hipError_t launch_score_s(const PageSelectArgs& a, int d, int gp, dim3 grid, hipStream_t s) {
-  if (d == 64) hipLaunchKernelGGL((score_kernel<E, 64, SHARE>), grid, dim3(64 * SW), 0, s, a, gp);
-  else if (d == 128) hipLaunchKernelGGL((score_kernel<E, 128, SHARE>), grid, dim3(64 * SW), 0, s, a, gp);
-  else hipLaunchKernelGGL((score_kernel<E, 256, SHARE>), grid, dim3(64 * SW), 0, s, a, gp);
+template <typename E, int D> hipError_t launch_score_d(const PageSelectArgs& a, hipStream_t s) {
+  // More rows than requests: some request has several rows, which can share
+  // its pages.  Otherwise (or with more heads than a tile) a row at a time.
+  if (a.R > a.B && a.G <= 16) {
+    int gp = 1;
+    while (gp < a.G) gp <<= 1;
+    const unsigned per = tiles_of_wave(gp) * SW * (16 / gp), gx = (a.R + per - 1) / per;
+    const unsigned want = (512 + gx * a.Hkv - 1) / (gx * a.Hkv), most = (a.NB + 127) / 128;
+    const dim3 grid(gx, a.Hkv, want < most ? want : most);
+    switch (gp) {
+      case 1: hipLaunchKernelGGL((score_rows_kernel<E, D, 1>), grid, dim3(64 * SW), 0, s, a); break;
+      case 2: hipLaunchKernelGGL((score_rows_kernel<E, D, 2>), grid, dim3(64 * SW), 0, s, a); break;
+      case 4: hipLaunchKernelGGL((score_rows_kernel<E, D, 4>), grid, dim3(64 * SW), 0, s, a); break;
+      case 8: hipLaunchKernelGGL((score_rows_kernel<E, D, 8>), grid, dim3(64 * SW), 0, s, a); break;
+      default: hipLaunchKernelGGL((score_rows_kernel<E, D, 16>), grid, dim3(64 * SW), 0, s, a); break;
+    }
+    return hipGetLastError();
+  }
+  const int hs = a.Hkv >= 4 ? 4 : a.Hkv >= 2 ? 2 : 1, hb = (a.Hkv + hs - 1) / hs;
+  const long long rh = (long long)a.R * hb;
+  const long long want = (1024 + rh - 1) / rh, most = (a.NB + 64 * (SW / hs) - 1) / (64 * (SW / hs));
+  const int z = (int)(want < most ? want : most);
+  const long long units = ((long long)a.R * z + 7) / 8 * 8;
+  hipLaunchKernelGGL((score_row_kernel<E, D>), dim3((unsigned)(units * hb)), dim3(64 * SW), 0, s, a, hs, z);
   return hipGetLastError();
 }
 
 template <typename E> hipError_t launch_score(const PageSelectArgs& a, int d, hipStream_t s) {
-  // Rows that share requests (more rows than requests) fill a tile; a row of
-  // its own request takes one alone, so that no wave walks several tables.
-  const bool share = a.R > a.B;
-  int gp = 16;
-  if (share)
-    for (gp = 1; gp < a.G && gp < 16;) gp <<= 1;
-  const int tt = 16 / gp;
-  const long long tiles = ((long long)a.R + tt - 1) / tt;
-  const long long gx = share ? (tiles + SW - 1) / SW : tiles;
-  // page splits: enough workgroups for the chip, each wave its four page groups
-  const int run = share ? 64 : 64 * SW;
-  const long long most = (a.NB + run - 1) / run, want = (2048 + gx * a.Hkv - 1) / (gx * a.Hkv);
-  const dim3 grid((unsigned)gx, a.Hkv, (unsigned)(want < most ? want : most));
-  return share ? launch_score_s<E, true>(a, d, gp, grid, s) : launch_score_s<E, false>(a, d, gp, grid, s);
+  if (d == 64) return launch_score_d<E, 64>(a, s);
+  if (d == 128) return launch_score_d<E, 128>(a, s);
+  return launch_score_d<E, 256>(a, s);
 }
 
 }  // namespace
@@ -290,12 +513,17 @@ hipError_t launch_paged_select(const PageSelectArgs& a, int dtype, int d, hipStr
   if (a.NB > a.K)                                      // otherwise no row has a choice
     e = dtype == 1 ? launch_score<bf16>(a, d, s) : dtype == 2 ? launch_score<fp16>(a, d, s) : launch_score<float>(a, d, s);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((size_t)a.R * a.Hkv));
-  if (a.NB <= 64) hipLaunchKernelGGL((pick_kernel<64, 1>), grid, dim3(64), 0, s, a);
-  else if (a.NB <= 256) hipLaunchKernelGGL((pick_kernel<64, 4>), grid, dim3(64), 0, s, a);
-  else if (a.NB <= 1024) hipLaunchKernelGGL((pick_kernel<256, 4>), grid, dim3(256), 0, s, a);
-  else if (a.NB <= 4096) hipLaunchKernelGGL((pick_kernel<256, 16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((pick_kernel<1024, 16>), grid, dim3(1024), 0, s, a);
+  // One wave for each row while it holds the scores in 4 registers, or in 16
+  // where the rows alone fill the chip; else as many waves as that takes.
+  const long long rows = (long long)a.R * a.Hkv;
+  const dim3 many((unsigned)rows), four((unsigned)((rows + 3) / 4));
+  if (a.NB <= 64) hipLaunchKernelGGL((pick_kernel<1, 1>), four, dim3(256), 0, s, a);
+  else if (a.NB <= 256) hipLaunchKernelGGL((pick_kernel<1, 4>), four, dim3(256), 0, s, a);
+  else if (a.NB <= 1024 && rows >= 4096) hipLaunchKernelGGL((pick_kernel<1, 16>), four, dim3(256), 0, s, a);
+  else if (a.NB <= 1024) hipLaunchKernelGGL((pick_kernel<4, 4>), many, dim3(256), 0, s, a);
+  else if (a.NB <= 2048) hipLaunchKernelGGL((pick_kernel<4, 8>), many, dim3(256), 0, s, a);
+  else if (a.NB <= 4096) hipLaunchKernelGGL((pick_kernel<4, 16>), many, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((pick_kernel<16, 16>), many, dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

@@ -515,16 +515,20 @@ PLAN_REFUSED = {"pages": 1, "width": 2, "rows": 4, "negative": 8}   # codes of p
 class _On:
     """The call's device as the current one, and its stream."""
 
+    __slots__ = ("device", "away", "other", "stream", "raw")
+
     def __init__(self, device, stream):
         import torch
-        self.stream = self.current = torch.cuda.current_stream(device)
-        self.other = stream is not None and stream != self.current
+        index = device.index
+        self.device = device
+        self.away = index != torch._C._cuda_getDevice()
+        self.raw = torch._C._cuda_getCurrentRawStream(index)
+        self.other = stream is not None and stream.cuda_stream != self.raw
         if self.other:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
             self.stream = stream
-        self.device = device
-        self.away = device.index != torch.cuda.current_device()
+            self.raw = stream.cuda_stream
 
     def empty(self, shape, dtype):
         """Memory that belongs to the call's stream, held for the current one too."""
@@ -533,7 +537,7 @@ class _On:
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
             t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(self.current)
+        t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def call(self, name, *args, hold=()):
@@ -541,9 +545,9 @@ class _On:
         if self.away:
             import torch
             with torch.cuda.device(self.device):
-                st = fn(*args, self.stream.cuda_stream)
+                st = fn(*args, self.raw)
         else:
-            st = fn(*args, self.stream.cuda_stream)
+            st = fn(*args, self.raw)
         if st != 0:
             raise SgdnError(st, name)
         if self.other:
@@ -552,50 +556,48 @@ class _On:
                     t.record_stream(self.stream)
 
 
-def _dev_check(device, **tensors):
-    """Contiguous device tensors of one device; a name ending in a type's letter
-    (``_i``, ``_l``, ``_f``, ``_b``, ``_u``) asks for that element type."""
-    import torch
-    kinds = {"_i": torch.int32, "_l": torch.int64, "_f": torch.float32, "_b": torch.int8,
-             "_u": torch.uint8}
-    for name, t in tensors.items():
+def _paged_check(device, *tensors):
+    """Each (name, tensor or None, element type or None, shape or None): a contiguous
+    tensor of the call's device.  One pass, as it is much of a small call's time."""
+    for name, t, dtype, shape in tensors:
         if t is None:
             continue
-        dtype = kinds.get(name[-2:])
-        if dtype is not None:
-            name = name[:-2]
-        _check(t, name, dtype)
-        if t.device != device:
+        if (t.device != device or (dtype is not None and t.dtype is not dtype)
+                or not t.is_contiguous() or not t.is_cuda):
+            _check(t, name, dtype)
             raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
-def _shape_check(name, t, shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _row_view(t, name, device, dtype):
-    """[R, heads, d] whose rows are contiguous; returns its row stride."""
+def _row_view(t, name, device, dtype, shape):
+    """[R, heads, d] whose rows are contiguous; returns its row stride.  ``shape``: None
+    where any size will do."""
     if t.dim() != 3:
         raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     rows, heads, d = t.shape
+    if t.shape != shape and any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if rows == 0:
+        return heads * d
     ld, sh, se = t.stride()
-    if rows > 1 and ld < heads * d or (heads > 1 and sh != d) or (d > 1 and se != 1):
+    if (rows > 1 and ld < heads * d) or (heads > 1 and sh != d) or (d > 1 and se != 1):
         raise ValueError(f"each row of {name} must be contiguous, got strides {t.stride()}")
     return ld if rows > 1 else heads * d
 
 
 def _paged(rows, q_heads, cache_shape, dtype, out_dtype=None, batch=1, width=1, max_len=None):
     n_pages, n_kv, page, d = cache_shape
+    code = _ocode(dtype)
     return Paged(rows, batch, q_heads, n_kv, d, page, n_pages, width,
-                 0 if max_len is None else int(max_len), _ocode(dtype),
-                 _ocode(dtype if out_dtype is None else out_dtype))
+                 0 if max_len is None else int(max_len), code,
+                 code if out_dtype is None else _ocode(out_dtype))
 
 
 def paged_workspace_bytes(shape: Paged, n_blocks=0, select=False) -> int:
@@ -604,16 +606,29 @@ def paged_workspace_bytes(shape: Paged, n_blocks=0, select=False) -> int:
 
 
 def _paged_ws(shape, n_blocks, select, on, workspace):
+    """(pointer, bytes, tensor) of the call's workspace."""
     nbytes = paged_workspace_bytes(shape, n_blocks, select)
     if nbytes == 0:
         raise SgdnError(-2, "sgdn_paged_workspace_bytes")
-    if workspace is not None:
-        _dev_check(on.device, workspace=workspace)
-        if workspace.numel() * workspace.element_size() < nbytes:
-            raise SgdnError(-3, "workspace")
-        return workspace, workspace.numel() * workspace.element_size()
     import torch
-    return on.empty(nbytes, torch.uint8), nbytes
+    if workspace is None:
+        if nbytes <= 256:                  # none is used
+            return None, 0, None
+        workspace = on.empty(nbytes, torch.uint8)
+    else:
+        _paged_check(on.device, ("workspace", workspace, None, None))
+        nbytes = workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), nbytes, workspace
+
+
+def _optional(t):
+    return None if t is None else t.data_ptr()
+
+
+def _table_shape(table):
+    if table.dim() != 2:
+        raise ValueError("table must be [B, W]")
+    return table.shape
 
 
 def paged_release(lens, done, table, free_list, free_pos, page, lens_out=None, free_pos_out=None,
@@ -625,25 +640,21 @@ def paged_release(lens, done, table, free_list, free_pos, page, lens_out=None, f
     (updated in place), by default new tensors.
     """
     import torch
-    dev = lens.device
-    _dev_check(dev, lens_i=lens, done_u=done, table_i=table, free_list_i=free_list,
-               free_pos_l=free_pos, lens_out_i=lens_out, free_pos_out_l=free_pos_out)
-    if table.dim() != 2:
-        raise ValueError("table must be [B, W]")
-    B, W = table.shape
+    dev, i32, i64 = lens.device, torch.int32, torch.int64
+    B, W = _table_shape(table)
+    _paged_check(dev, ("lens", lens, i32, (B,)), ("done", done, torch.uint8, (B,)),
+                 ("table", table, i32, None), ("free_list", free_list, i32, None),
+                 ("free_pos", free_pos, i64, (2,)), ("lens_out", lens_out, i32, (B,)),
+                 ("free_pos_out", free_pos_out, i64, (2,)))
     on = _On(dev, stream)
     if lens_out is None:
-        lens_out = on.empty((B,), torch.int32)
+        lens_out = on.empty((B,), i32)
     if free_pos_out is None:
-        free_pos_out = on.empty((2,), torch.int64)
-    for n, t, shape in (("lens", lens, (B,)), ("done", done, (B,)), ("free_pos", free_pos, (2,)),
-                        ("lens_out", lens_out, (B,)), ("free_pos_out", free_pos_out, (2,))):
-        _shape_check(n, t, shape)
-    on.call(
-        "sgdn_paged_release", B, page, W, free_list.numel(), lens.data_ptr(), done.data_ptr(),
-        table.data_ptr(), free_list.data_ptr(), free_pos.data_ptr(), lens_out.data_ptr(),
-        free_pos_out.data_ptr(),
-        hold=(lens, done, table, free_list, free_pos, lens_out, free_pos_out))
+        free_pos_out = on.empty((2,), i64)
+    on.call("sgdn_paged_release", B, page, W, free_list.numel(), lens.data_ptr(), done.data_ptr(),
+            table.data_ptr(), free_list.data_ptr(), free_pos.data_ptr(), lens_out.data_ptr(),
+            free_pos_out.data_ptr(),
+            hold=(lens, done, table, free_list, free_pos, lens_out, free_pos_out))
     return lens_out, free_pos_out
 
 
@@ -658,44 +669,39 @@ def paged_plan(lens, add, table, free_list, free_pos, page, rows, lens_out=None,
     ``out`` reuses the dict of an earlier call of the same sizes.
     """
     import torch
-    dev = lens.device
-    _dev_check(dev, lens_i=lens, add_i=add, table_i=table, free_list_i=free_list,
-               free_pos_l=free_pos, lens_out_i=lens_out, free_pos_out_l=free_pos_out)
-    if table.dim() != 2:
-        raise ValueError("table must be [B, W]")
-    B, W = table.shape
+    dev, i32, i64 = lens.device, torch.int32, torch.int64
+    B, W = _table_shape(table)
     rows = int(rows)
     if rows < 0:
         raise ValueError(f"rows must not be negative, got {rows}")
+    _paged_check(dev, ("lens", lens, i32, (B,)), ("add", add, i32, (B,)),
+                 ("table", table, i32, None), ("free_list", free_list, i32, None),
+                 ("free_pos", free_pos, i64, (2,)), ("lens_out", lens_out, i32, (B,)),
+                 ("free_pos_out", free_pos_out, i64, (2,)))
     on = _On(dev, stream)
-    sizes = dict(cu=B + 1, page_cu=B + 1, slot=rows, row_req=rows, row_len=rows, status=B)
     if out is None:
-        own = on.empty((sum(sizes.values()) + B,), torch.int32)
-        parts = own.split([*sizes.values(), B])
-        out = dict(zip(sizes, parts))
-        out["lens"] = parts[-1] if lens_out is None else lens_out
-        out["free_pos"] = on.empty((2,), torch.int64) if free_pos_out is None else free_pos_out
+        cu, page_cu, slot, row_req, row_len, status, new = on.empty(
+            (4 * B + 2 + 3 * rows,), i32).split((B + 1, B + 1, rows, rows, rows, B, B))
+        out = dict(cu=cu, page_cu=page_cu, slot=slot, row_req=row_req, row_len=row_len,
+                   status=status, lens=new if lens_out is None else lens_out,
+                   free_pos=on.empty((2,), i64) if free_pos_out is None else free_pos_out)
     else:
         out = dict(out)
-        for n, size in sizes.items():
-            _dev_check(dev, **{n + "_i": out[n]})
-            _shape_check(n, out[n], (size,))
         if lens_out is not None:
             out["lens"] = lens_out
         if free_pos_out is not None:
             out["free_pos"] = free_pos_out
-        _dev_check(dev, lens_i=out["lens"], free_pos_l=out["free_pos"])
-    for n, t, shape in (("lens", lens, (B,)), ("add", add, (B,)), ("free_pos", free_pos, (2,)),
-                        ("lens_out", out["lens"], (B,)), ("free_pos_out", out["free_pos"], (2,))):
-        _shape_check(n, t, shape)
+        _paged_check(dev, *((n, out[n], i32, (size,)) for n, size in
+                            (("cu", B + 1), ("page_cu", B + 1), ("slot", rows), ("row_req", rows),
+                             ("row_len", rows), ("status", B), ("lens", B))),
+                     ("free_pos", out["free_pos"], i64, (2,)))
     o = out
-    on.call(
-        "sgdn_paged_plan", B, page, W, rows, free_list.numel(), lens.data_ptr(), add.data_ptr(),
-        table.data_ptr(), free_list.data_ptr(), free_pos.data_ptr(), o["lens"].data_ptr(),
-        o["free_pos"].data_ptr(), o["cu"].data_ptr(), o["page_cu"].data_ptr(),
-        o["slot"].data_ptr(), o["row_req"].data_ptr(), o["row_len"].data_ptr(),
-        o["status"].data_ptr(),
-        hold=(lens, add, table, free_list, free_pos, *o.values()))
+    on.call("sgdn_paged_plan", B, page, W, rows, free_list.numel(), lens.data_ptr(),
+            add.data_ptr(), table.data_ptr(), free_list.data_ptr(), free_pos.data_ptr(),
+            o["lens"].data_ptr(), o["free_pos"].data_ptr(), o["cu"].data_ptr(),
+            o["page_cu"].data_ptr(), o["slot"].data_ptr(), o["row_req"].data_ptr(),
+            o["row_len"].data_ptr(), o["status"].data_ptr(),
+            hold=(lens, add, table, free_list, free_pos, *o.values()))
     return out
 
 
@@ -707,84 +713,62 @@ def paged_write(k, v, slot, k_cache, v_cache, codes=None, code_scale=None, strea
     [n_pages, Hkv] the pages that the rows complete are summarised there, for
     ``paged_select``.
     """
+    import torch
     dev, dt = k_cache.device, k_cache.dtype
-    _dev_check(dev, slot_i=slot, k_cache=k_cache, v_cache=v_cache, codes_b=codes,
-               code_scale_f=code_scale)
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [n_pages, Hkv, page, d]")
-    ldk, ldv = _row_view(k, "k", dev, dt), _row_view(v, "v", dev, dt)
     n_pages, n_kv, page, d = k_cache.shape
     rows = k.shape[0]
-    if v_cache.dtype != dt:
-        raise ValueError(f"v_cache must be {dt}, got {v_cache.dtype}")
-    for n, t, shape in (("v_cache", v_cache, (n_pages, n_kv, page, d)), ("k", k, (rows, n_kv, d)),
-                        ("v", v, (rows, n_kv, d)), ("slot", slot, (rows,)),
-                        ("codes", codes, (n_pages, n_kv, d)),
-                        ("code_scale", code_scale, (n_pages, n_kv))):
-        _shape_check(n, t, shape)
-    shape = _paged(rows, n_kv, (n_pages, n_kv, page, d), dt)
+    _paged_check(dev, ("slot", slot, torch.int32, (rows,)), ("k_cache", k_cache, None, None),
+                 ("v_cache", v_cache, dt, k_cache.shape),
+                 ("codes", codes, torch.int8, (n_pages, n_kv, d)),
+                 ("code_scale", code_scale, torch.float32, (n_pages, n_kv)))
+    ldk = _row_view(k, "k", dev, dt, (rows, n_kv, d))
+    ldv = _row_view(v, "v", dev, dt, (rows, n_kv, d))
+    shape = _paged(rows, n_kv, k_cache.shape, dt)
     _On(dev, stream).call(
         "sgdn_paged_write", ctypes.byref(shape), k.data_ptr(), v.data_ptr(), ldk, ldv,
-        slot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        None if codes is None else codes.data_ptr(),
-        None if code_scale is None else code_scale.data_ptr(),
-        hold=(k, v, slot, k_cache, v_cache, codes, code_scale))
-
-
-def _paged_rows(q, table, row_len, row_req, dev):
-    """Checks what the reading calls share; returns (rows, batch, width)."""
-    _dev_check(dev, table_i=table, row_len_i=row_len, row_req_i=row_req)
-    if table.dim() != 2:
-        raise ValueError("table must be [B, W]")
-    rows = q.shape[0]
-    _shape_check("row_len", row_len, (rows,))
-    _shape_check("row_req", row_req, (rows,))
-    if row_req is None and rows > table.shape[0]:
-        raise ValueError("without row_req, row r is request r: more rows than requests")
-    return rows, table.shape[0], table.shape[1]
+        slot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _optional(codes),
+        _optional(code_scale), hold=(k, v, slot, k_cache, v_cache, codes, code_scale))
 
 
 def _attend(name, q, k_cache, v_cache, table, row_len, row_req, blocks, scale, max_len, o,
             out_dtype, want_lse, lse, workspace, stream):
     import torch
-    dev, dt = k_cache.device, k_cache.dtype
-    ldq = _row_view(q, "q", dev, dt)
-    if o is not None:
-        out_dtype = o.dtype
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
-    _dev_check(dev, k_cache=k_cache, v_cache=v_cache, blocks_i=blocks, o=o, lse_f=lse)
+    dev, dt, i32 = k_cache.device, k_cache.dtype, torch.int32
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [n_pages, Hkv, page, d]")
-    if v_cache.dtype != dt:
-        raise ValueError(f"v_cache must be {dt}, got {v_cache.dtype}")
-    _shape_check("v_cache", v_cache, tuple(k_cache.shape))
-    rows, B, W = _paged_rows(q, table, row_len, row_req, dev)
-    n_q, d = q.shape[1], q.shape[2]
-    if d != k_cache.shape[3]:
-        raise ValueError(f"q has heads of {d}, the cache of {k_cache.shape[3]}")
-    _shape_check("o", o, (rows, n_q, d))
-    _shape_check("lse", lse, (rows, n_q))
-    n_blocks = 0
+    n_kv, d = k_cache.shape[1], k_cache.shape[3]
+    ldq = _row_view(q, "q", dev, dt, (None, None, d))
+    rows, n_q, _ = q.shape
+    B, W = _table_shape(table)
+    n_blocks, lists = 0, ()
     if blocks is not None:
         if blocks.dim() != 3 or blocks.shape[2] < 1:
             raise ValueError("blocks must be [R, Hkv, n_blocks]")
         n_blocks = blocks.shape[2]
-        _shape_check("blocks", blocks, (rows, k_cache.shape[1], n_blocks))
+        lists = (blocks.data_ptr(), n_blocks)
+    if row_req is None and rows > B:
+        raise ValueError("without row_req, row r is request r: more rows than requests")
+    if o is not None:
+        out_dtype = o.dtype
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    _paged_check(dev, ("k_cache", k_cache, None, None), ("v_cache", v_cache, dt, k_cache.shape),
+                 ("table", table, i32, None), ("row_len", row_len, i32, (rows,)),
+                 ("row_req", row_req, i32, (rows,)),
+                 ("blocks", blocks, i32, (rows, n_kv, n_blocks)),
+                 ("o", o, None, (rows, n_q, d)), ("lse", lse, torch.float32, (rows, n_q)))
     shape = _paged(rows, n_q, k_cache.shape, dt, out_dtype, B, W, max_len)
     on = _On(dev, stream)
-    ws, nbytes = _paged_ws(shape, n_blocks, False, on, workspace)
+    ws, nbytes, held = _paged_ws(shape, n_blocks, False, on, workspace)
     if o is None:
         o = on.empty((rows, n_q, d), out_dtype)
     if want_lse and lse is None:
         lse = on.empty((rows, n_q), torch.float32)
-    if scale is None:
-        scale = d ** -0.5
-    lists = () if blocks is None else (blocks.data_ptr(), n_blocks)
     on.call(name, ctypes.byref(shape), q.data_ptr(), ldq, k_cache.data_ptr(), v_cache.data_ptr(),
-            table.data_ptr(), None if row_req is None else row_req.data_ptr(),
-            row_len.data_ptr(), *lists, float(scale), o.data_ptr(),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), nbytes,
-            hold=(q, k_cache, v_cache, table, row_req, row_len, blocks, o, lse, ws))
+            table.data_ptr(), _optional(row_req), row_len.data_ptr(), *lists,
+            d ** -0.5 if scale is None else float(scale), o.data_ptr(), _optional(lse), ws, nbytes,
+            hold=(q, k_cache, v_cache, table, row_req, row_len, blocks, o, lse, held))
     return o, lse
 
 
@@ -823,25 +807,27 @@ def paged_select(q, codes, code_scale, table, row_len, page, n_blocks, row_req=N
     row's first ``n_sink`` and last ``n_local`` blocks are always among them.
     """
     import torch
-    dev = codes.device
-    _dev_check(dev, codes_b=codes, code_scale_f=code_scale, blocks_i=blocks)
+    dev, i32 = codes.device, torch.int32
     if codes.dim() != 3:
         raise ValueError("codes must be [n_pages, Hkv, d]")
     n_pages, n_kv, d = codes.shape
-    _shape_check("code_scale", code_scale, (n_pages, n_kv))
-    ldq = _row_view(q, "q", dev, q.dtype)
-    rows, B, W = _paged_rows(q, table, row_len, row_req, dev)
-    if q.shape[2] != d:
-        raise ValueError(f"q has heads of {q.shape[2]}, the summaries of {d}")
-    _shape_check("blocks", blocks, (rows, n_kv, n_blocks))
+    ldq = _row_view(q, "q", dev, q.dtype, (None, None, d))
+    rows = q.shape[0]
+    B, W = _table_shape(table)
+    if row_req is None and rows > B:
+        raise ValueError("without row_req, row r is request r: more rows than requests")
+    _paged_check(dev, ("codes", codes, torch.int8, None),
+                 ("code_scale", code_scale, torch.float32, (n_pages, n_kv)),
+                 ("table", table, i32, None), ("row_len", row_len, i32, (rows,)),
+                 ("row_req", row_req, i32, (rows,)),
+                 ("blocks", blocks, i32, (rows, n_kv, n_blocks)))
     shape = _paged(rows, q.shape[1], (n_pages, n_kv, page, d), q.dtype, None, B, W, max_len)
     on = _On(dev, stream)
-    ws, nbytes = _paged_ws(shape, n_blocks, True, on, workspace)
+    ws, nbytes, held = _paged_ws(shape, n_blocks, True, on, workspace)
     if blocks is None:
-        blocks = on.empty((rows, n_kv, n_blocks), torch.int32)
+        blocks = on.empty((rows, n_kv, n_blocks), i32)
     on.call("sgdn_paged_select", ctypes.byref(shape), q.data_ptr(), ldq, codes.data_ptr(),
-            code_scale.data_ptr(), table.data_ptr(),
-            None if row_req is None else row_req.data_ptr(), row_len.data_ptr(), n_blocks, n_sink,
-            n_local, blocks.data_ptr(), ws.data_ptr(), nbytes,
-            hold=(q, codes, code_scale, table, row_req, row_len, blocks, ws))
+            code_scale.data_ptr(), table.data_ptr(), _optional(row_req), row_len.data_ptr(),
+            n_blocks, n_sink, n_local, blocks.data_ptr(), ws, nbytes,
+            hold=(q, codes, code_scale, table, row_req, row_len, blocks, held))
     return blocks

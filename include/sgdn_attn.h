@@ -143,8 +143,8 @@ int sgdn_paged_write(const sgdn_paged* p, const void* k, const void* v, int64_t 
 
 /* Device workspace of sgdn_paged_attend (n_blocks = 0), of
  * sgdn_paged_attend_sparse (n_blocks > 0, select = 0) and of
- * sgdn_paged_select (select = 1).  0 for an invalid shape; a valid one that
- * needs no memory gives 256. */
+ * sgdn_paged_select (select = 1).  0 for an invalid shape; 256 for a valid
+ * one that uses none, where ws may be NULL (ws_bytes is then not looked at). */
 size_t sgdn_paged_workspace_bytes(const sgdn_paged* p, int32_t n_blocks, int32_t select);
 
 /* o[r, h] = sum_t softmax_t(scale q[r, h] . k[t, h']) v[t, h'] over the

@@ -200,7 +200,7 @@ def test_attend_lowest_and_infinite_values():
 def test_attend_strided_q_and_given_outputs():
     import torch
     from gated_deltanet_prefill_chunkwise_amd import ops
-    c = Case(61, [100, 33, 64], 4, 2, 128, 64, "bf16")
+    c = Case(61, [1000, 33, 64], 4, 2, 128, 64, "bf16")
     fused = c.g(c.rng.standard_normal((3, 4 + 2 + 2, 128)))
     q = fused[:, :4]
     assert not q.is_contiguous()
@@ -359,7 +359,7 @@ def test_select(Hq, Hkv, D, G_note, dtype, coarse):
         assert np.array_equal(got.cpu().numpy(), want), (K, sink, local)
 
 
-@pytest.mark.parametrize("W", [64, 65, 256, 257, 1024, 1025, 4096, 4097, 16384])
+@pytest.mark.parametrize("W", [64, 65, 256, 257, 1024, 1025, 2048, 2049, 4096, 4097, 16384])
 def test_select_widths(W):
     """Every size class of the choice, at its borders."""
     import torch

@@ -126,7 +126,7 @@ def test_attend_arguments(L):
             assert _attend(L, sparse=sparse, ldq=ldq) == EINVAL
         assert _attend(L, _shape(o_dtype=5), sparse=sparse) == EINVAL
         assert _attend(L, _shape(rows=5), sparse=sparse, req=None) == EINVAL   # row r is request r
-        assert _attend(L, sparse=sparse, ws_bytes=255) == EWORKSPACE
+        assert _attend(L, sparse=sparse, ws_bytes=256) == EWORKSPACE
         assert _attend(L, _shape(rows=0), sparse=sparse, q=None, o=None) == 0  # nothing to do
     assert _attend(L, sparse=True, n_blocks=0) == EINVAL
     assert _attend(L, sparse=True, n_blocks=4097) == EUNSUPPORTED
