@@ -23,7 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "intra.hip", "hscan.hip", "ochunk.hip", "misc.hip", "select.hip",
            "decode.hip", "paged_api.hip", "paged_plan.hip", "paged_write.hip", "paged_attend.hip",
-           "paged_select.hip"]
+           "paged_select.hip", "paged_tiles.hip"]
 # hscan: products accumulate in ordinary vector registers (its state tiles are
 # also scaled and converted by vector instructions every event)
 EXTRA = {"select.hip": ["-ffp-contract=off"],

@@ -65,6 +65,8 @@ struct PageAttendArgs {
   int R, B, Hq, Hkv, G, MT;  // MT = ceil(G / 16) head tiles of a group
   int lp, n_pages, W, max_len, n_blocks, S;
   float scale;               // of the scores, times log2(e)
+  int32_t* done;             // [tiles][Hkv]: 1 where the tile kernel has made a tile's rows; NULL: no tiles
+  int TQ;                    // rows of a tile
 };
 
 struct PageSelectArgs {
@@ -88,6 +90,9 @@ hipError_t launch_paged_write(const PageWriteArgs& a, int dtype, int d, hipStrea
 // S of PageAttendArgs: `units` (row, head, head tile), `tiles` of 32 keys, bytes of a key row
 int paged_splits(long long units, int tiles, int row_bytes);
 hipError_t launch_paged_attend(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
+// Rows of a tile of launch_paged_tiles, 0 where it is not used.
+int paged_tile_rows(int R, int B, int G, int Hkv, bool has_req, int dtype, int lp, int max_len, int n_blocks);
+hipError_t launch_paged_tiles(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 hipError_t launch_paged_select(const PageSelectArgs& a, int dtype, int d, hipStream_t s);
 
 }  // namespace sgdn

@@ -61,9 +61,9 @@ int longest(const sgdn_paged* p) { return p->max_len > 0 ? p->max_len : p->width
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-struct AttendPlan { int S, MT; size_t off_ml, total; };
+struct AttendPlan { int S, MT, TQ; size_t off_ml, total; };
 
-AttendPlan attend_plan(const sgdn_paged* p, int n_blocks) {
+AttendPlan attend_plan(const sgdn_paged* p, int n_blocks, bool has_req) {
   AttendPlan pl;
   const int G = p->n_q / p->n_kv;
   pl.MT = (G + 15) / 16;
@@ -76,6 +76,11 @@ AttendPlan attend_plan(const sgdn_paged* p, int n_blocks) {
     pl.off_ml = align256(parts * p->d * sizeof(float));
     pl.total = pl.off_ml + align256(parts * 2 * sizeof(float));
   }
+  pl.TQ = 0;
+  if (n_blocks > 0 && pl.S == 1 && p->rows > 0)
+    pl.TQ = paged_tile_rows(p->rows, p->batch, G, p->n_kv, has_req, p->dtype, log2_page(p->page), longest(p), n_blocks);
+  if (pl.TQ > 0)
+    pl.total = NO_WORKSPACE + align256((size_t)((p->rows + pl.TQ - 1) / pl.TQ) * p->n_kv * sizeof(int32_t));
   if (pl.total == 0) pl.total = NO_WORKSPACE;
   return pl;
 }
@@ -100,7 +105,7 @@ int attend(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache,
   if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(o) || misaligned(ws))
     return SGDN_EINVAL;
   if (bad_stride(ldq, (int64_t)p->n_q * p->d, p->dtype)) return SGDN_EINVAL;
-  const AttendPlan pl = attend_plan(p, n_blocks);
+  const AttendPlan pl = attend_plan(p, n_blocks, row_req != nullptr);
   if (pl.total > NO_WORKSPACE && !ws) return SGDN_EINVAL;
   if (pl.total > NO_WORKSPACE && ws_bytes < pl.total) return SGDN_EWORKSPACE;
   PageAttendArgs a;
@@ -113,6 +118,10 @@ int attend(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache,
   a.lp = log2_page(p->page); a.n_pages = p->n_pages; a.W = p->width; a.max_len = longest(p);
   a.n_blocks = n_blocks; a.S = pl.S;
   a.scale = scale * 1.4426950408889634f;
+  a.TQ = pl.TQ;
+  a.done = pl.TQ > 0 ? static_cast<int32_t*>(ws) : nullptr;
+  if (pl.TQ > 0 && launch_paged_tiles(a, p->dtype, p->o_dtype, p->d, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return SGDN_EHIP;
   return launch_paged_attend(a, p->dtype, p->o_dtype, p->d, static_cast<hipStream_t>(stream)) == hipSuccess
              ? SGDN_OK : SGDN_EHIP;
 }
@@ -168,7 +177,7 @@ int sgdn_paged_write(const sgdn_paged* p, const void* k, const void* v, int64_t 
 
 size_t sgdn_paged_workspace_bytes(const sgdn_paged* p, int32_t n_blocks, int32_t select) {
   if (check_read(p) != SGDN_OK || n_blocks < 0 || n_blocks > MAX_LIST) return 0;
-  if (select == 0) return attend_plan(p, n_blocks).total;
+  if (select == 0) return attend_plan(p, n_blocks, true).total;   // without row_req no more
   if (n_blocks < 1 || (longest(p) + p->page - 1) / p->page > MAX_NB) return 0;
   return select_bytes(p, n_blocks);
 }

@@ -97,6 +97,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
   const int mt = unit % a.MT;
   const int rh = unit / a.MT;
   const int h = rh / a.R, row = rh - h * a.R;
+  if (SPARSE && a.done != nullptr && a.done[(size_t)(row / a.TQ) * a.Hkv + h] != 0) return;   // made with its tile
   const int req = a.row_req == nullptr ? row : a.row_req[row];
   const int P = 1 << a.lp;
   int len = min(a.row_len[row], a.max_len);
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         const float cn = fmaxf(c, mx - BIAS);
-        const float f = cn == -INFINITY ? 1.f : exp2f(c - cn);
+        const float f = cn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(c - cn);
         c = cn;
         l *= f;
 #pragma unroll
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
       const float cs = c == -INFINITY ? 0.f : c;           // every x so far is -inf
       f32x8 p;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) { p[j] = exp2f(x[j] - cs); l += p[j]; }
+      for (int j = 0; j < 8; ++j) { p[j] = __builtin_amdgcn_exp2f(x[j] - cs); l += p[j]; }
       frag_t<E> ph, pl;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
   float top = -INFINITY;
 #pragma unroll
   for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][n][0]);
-  const float mine = c == -INFINITY ? 0.f : exp2f(c - top);
+  const float mine = c == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(c - top);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
     for (int w = 0; w < NW; ++w) {
       const float lw = ml[w][hd][1], cw = ml[w][hd][0];
       any = any || !(lw == -1.f);
-      if (cw != -INFINITY) sum += lw * exp2f(cw - m);
+      if (cw != -INFINITY) sum += lw * __builtin_amdgcn_exp2f(cw - m);
       else if (!(lw <= 0.f)) sum = lw;                     // NaN
     }
     f32x4 o = zero4();
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(256) void join_kernel(PageAttendArgs a) {
 #pragma unroll
   for (int i = 0; i < MAX_SPLITS / 64; ++i) {
     any = any || !(l[i] == -1.f);
-    const float w = c[i] == -INFINITY ? 0.f : exp2f(c[i] - m);
+    const float w = c[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(c[i] - m);
     if (c[i] != -INFINITY) sum += l[i] * w;
     else if (!(l[i] <= 0.f)) sum += l[i];                  // NaN
     if (wave == 0) weight[64 * i + lane] = w;

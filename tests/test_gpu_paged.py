@@ -591,3 +591,99 @@ def test_binding_refusals():
         ops.paged_write(q[:, :2], q[:, 2:], n, c.k, c.v, codes)       # codes without their scale
     ops.paged_attend(q[:0], c.k, c.v, t, n[:0])                       # nothing to do
     torch.cuda.synchronize()
+
+
+# attend_sparse of prompts ----------------------------------------------------
+
+
+def _prompt(seed, Hq, Hkv, D, P, dtype, K, lens, new, nan=None, pad=3, alike=8):
+    """Every new token of the given requests as a row; lists that `alike` rows in a row mostly share."""
+    c = Case(seed, lens, Hq, Hkv, D, P, dtype)
+    req = np.r_[np.repeat(np.arange(len(lens)), new), -np.ones(pad)].astype(np.int32)
+    length = np.r_[np.concatenate([n - m + 1 + np.arange(m) for n, m in zip(lens, new)]), np.zeros(pad)].astype(np.int32)
+    R = len(req)
+    nb = -(-length // P)
+    lists = np.full((R, Hkv, K), -1, np.int32)
+    for r in range(R):
+        rng = np.random.default_rng([seed, r // alike])
+        for h in range(Hkv):
+            order = rng.permutation(max(int(nb.max()), 1))
+            pick = [j for j in order if j < nb[r]][:K - 1]
+            if nb[r] > 0 and c.rng.random() < 0.3 and pick:
+                pick[c.rng.integers(len(pick))] = int(nb[r]) - 1
+            if nb[r] > 0:
+                pick.append(int(nb[r]) - 1)
+            lists[r, h, :len(pick)] = sorted(pick) if K % 2 else pick   # a block may come twice
+    return c, req, length, lists, c.q(R)
+
+
+@pytest.mark.parametrize("dtype, out", [("bf16", "bf16"), ("f16", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("Hq, Hkv, D, P, K", [
+    (8, 1, 64, 16, 5), (8, 1, 128, 64, 3), (8, 1, 256, 32, 4), (16, 1, 64, 32, 6), (12, 1, 128, 16, 7),
+    (5, 1, 64, 64, 3), (2, 2, 64, 16, 9), (3, 1, 128, 128, 2), (2, 1, 64, 16, 4), (1, 1, 64, 32, 5)])
+def test_attend_sparse_prompts(Hq, Hkv, D, P, K, dtype, out):
+    """Tiles of rows that share lists: within a request, across a border, with padding rows behind."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    G = Hq // Hkv
+    gp = 1 << (G - 1).bit_length()
+    R = 128 * (128 // gp) // Hkv + 50              # as many tiles as it takes
+    new = [R - R // 3, R // 3 - 1, 1]
+    lens = np.array(new) + [70, 3, 200]
+    c, req, length, lists, q = _prompt(Hq + D + P, Hq, Hkv, D, P, dtype, K, lens, new)
+    t = [_i32(x) for x in (c.table, length, lists, req)]
+    o, lse = ops.paged_attend_sparse(q, c.k, c.v, t[0], t[1], t[2], row_req=t[3], out_dtype=_t(out), want_lse=True)
+    torch.cuda.synchronize()
+    rows = np.unique(np.r_[np.arange(0, 40), c.rng.integers(0, len(req), 60), new[0] - 20 + np.arange(40), len(req) - 30 + np.arange(30)])
+    want = ref.attend(_f64(q[rows]), _f64(c.k), _f64(c.v), c.table, length[rows], req[rows], blocks=lists[rows])
+    i = torch.from_numpy(rows).cuda()
+    check(o[i], lse[i], want, out, dtype, D)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-3, 3.0])
+def test_attend_scale(scale):
+    """Scales of either sign and 0, for single rows and for tiles of rows."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    R = 128 * 16 + 9
+    c, req, length, lists, q = _prompt(9, 8, 1, 64, 32, "bf16", 3, np.array([R + 60]), [R], pad=0)
+    t = [_i32(x) for x in (c.table, length, lists, req)]
+    rows = np.arange(0, R, 57)
+    i = torch.from_numpy(rows).cuda()
+    for n in (R, 40):
+        o, lse = ops.paged_attend_sparse(q[-n:], c.k, c.v, t[0], t[1][-n:], t[2][-n:], row_req=t[3][-n:], scale=scale, want_lse=True)
+        torch.cuda.synchronize()
+        pick = rows[rows >= R - n]
+        j = torch.from_numpy(pick - (R - n)).cuda()
+        want = ref.attend(_f64(q[torch.from_numpy(pick).cuda()]), _f64(c.k), _f64(c.v), c.table, length[pick], req[pick], scale, lists[pick])
+        check(o[j], lse[j], want, "f32", "bf16", 64)
+
+
+def test_attend_sparse_prompts_see_only_their_own():
+    """A row's result does not change with what other rows of its tile list or see: values
+    that are not finite in their blocks, in later tokens, or an infinite score of one."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    R = 128 * 16 + 9
+    c, req, length, lists, q = _prompt(5, 8, 1, 64, 16, "bf16", 4, np.array([R + 60]), [R], pad=0, alike=1)
+    t = [_i32(x) for x in (c.table, length, lists, req)]
+    call = lambda: ops.paged_attend_sparse(q, c.k, c.v, t[0], t[1], t[2], row_req=t[3], want_lse=True)
+    o, lse = call()
+    bad = c.table[0, [3, 40, 100]]
+    c.v[bad[0], 0, 5, 7], c.v[bad[1], 0, 2] = float("nan"), float("inf")
+    c.k[bad[2], 0, 9, 3] = float("inf")
+    o2, lse2 = call()
+    torch.cuda.synchronize()
+    hit = np.zeros(R, bool)
+    for j, place in ((3, 5), (40, 2), (100, 9)):
+        hit |= (lists[:, 0] == j).any(-1) & (length > 16 * j + place)
+    assert 0 < hit.sum() < R
+    clean = torch.from_numpy(~hit).cuda()
+    # the kernel for single rows sums in another order than the tiles: equal within both bounds
+    rows = np.flatnonzero(~hit)[::41]
+    want = ref.attend(_f64(q[rows]), np.nan_to_num(_f64(c.k)), np.nan_to_num(_f64(c.v)), c.table, length[rows], req[rows], blocks=lists[rows])
+    i = torch.from_numpy(rows).cuda()
+    check(o2[i], lse2[i], want, "f32", "bf16", 64)
+    check(o[i], lse[i], want, "f32", "bf16", 64)
+    assert torch.isfinite(o2[clean]).all() and torch.isfinite(o).all()
+    assert not torch.isfinite(o2[~clean].reshape(int(hit.sum()), -1)).all(-1).any()
