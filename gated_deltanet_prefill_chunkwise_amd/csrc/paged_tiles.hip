@@ -300,6 +300,26 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
                 s1[t] = mma(kf[2 * u + 1], qf[t][s + u], s1[t]);
               }
           }
+          const E* vb = stage + buf * BUF + SK * D;
+          const int k0 = 8 * g + (n >> 2);
+          auto value = [&](int d) {                       // 16 elements: 16-byte units 2d, 2d + 1
+            typedef short s16x8 __attribute__((ext_vector_type(8)));
+            const E* v0 = vb + k0 * D + 8 * v_unit<D>(k0, 2 * d) + 4 * (n & 3);
+            const E* v1 = vb + (k0 + 4) * D + 8 * v_unit<D>(k0 + 4, 2 * d) + 4 * (n & 3);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v0);
+            const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v1);
+            const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(frag_t<E>, v);
+          };
+          // The values' reads before the weights are formed, where the registers
+          // hold them that long (D = 128: 126 -> 118 us; D = 256 spills).
+          constexpr bool EARLY = D < 256;
+          frag_t<E> vf[DT];
+          if (EARLY) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vf[d] = value(d);
+            __builtin_amdgcn_sched_barrier(0);
+          }
           frag_t<E> ph[CT], pl[CT];
 #pragma unroll
           for (int t = 0; t < CT; ++t) {
@@ -335,17 +355,9 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
               if (TWO) pl[t][r] = from_f<E>(p - to_f(ph[t][r]));
             }
           }
-          const E* vb = stage + buf * BUF + SK * D;
-          const int k0 = 8 * g + (n >> 2);
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {                  // 16 elements: 16-byte units 2d, 2d + 1
-            typedef short s16x8 __attribute__((ext_vector_type(8)));
-            const E* v0 = vb + k0 * D + 8 * v_unit<D>(k0, 2 * d) + 4 * (n & 3);
-            const E* v1 = vb + (k0 + 4) * D + 8 * v_unit<D>(k0 + 4, 2 * d) + 4 * (n & 3);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v0);
-            const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v1);
-            const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
-            const frag_t<E> vt = __builtin_bit_cast(frag_t<E>, v);
+          for (int d = 0; d < DT; ++d) {
+            const frag_t<E> vt = EARLY ? vf[d] : value(d);
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
               acc[t][d] = mma(vt, ph[t], acc[t][d]);
