@@ -203,7 +203,7 @@ hipError_t launch_paged_plan(const PagePlanArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((plan_kernel<true>), dim3(1), dim3(n), 0, s, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((plan_kernel<false>), dim3(1), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL((plan_kernel<false>), dim3(1), dim3(a.B <= 256 ? 256 : 1024), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.R == 0) return e;
   hipLaunchKernelGGL(fill_kernel, dim3((a.R + 255) / 256), dim3(256), 0, s, a);

@@ -19,9 +19,7 @@ namespace sgdn {
 
 namespace {
 
-constexpr int TR = 16;
-
-template <typename E, int D>
+template <typename E, int D, int TR>
 __global__ __launch_bounds__(256) void write_kernel(PageWriteArgs a) {
   constexpr int EV = 16 / sizeof(E);        // elements of a 16-byte access
   constexpr int U = D / EV;                 // accesses per row
@@ -94,13 +92,21 @@ __global__ __launch_bounds__(256) void write_kernel(PageWriteArgs a) {
   }
 }
 
-template <typename E>
-hipError_t launch_write_e(const PageWriteArgs& a, int d, hipStream_t s) {
-  const dim3 grid((a.R + TR - 1) / TR, a.Hkv);
-  if (d == 64) hipLaunchKernelGGL((write_kernel<E, 64>), grid, dim3(256), 0, s, a);
-  else if (d == 128) hipLaunchKernelGGL((write_kernel<E, 128>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((write_kernel<E, 256>), grid, dim3(256), 0, s, a);
+// Rows of a workgroup: 8 for a few rows, where more workgroups end sooner
+// (128 rows of 8 heads of 128: 4.1 us against 5.0 with 16), else 16 (28,000
+// rows: 90 us against 100 with 8, 95 with 32, 102 with 64).
+template <typename E, int D> hipError_t launch_write_d(const PageWriteArgs& a, hipStream_t s) {
+  if (a.R <= 1024)
+    hipLaunchKernelGGL((write_kernel<E, D, 8>), dim3((a.R + 7) / 8, a.Hkv), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((write_kernel<E, D, 16>), dim3((a.R + 15) / 16, a.Hkv), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+
+template <typename E> hipError_t launch_write_e(const PageWriteArgs& a, int d, hipStream_t s) {
+  if (d == 64) return launch_write_d<E, 64>(a, s);
+  if (d == 128) return launch_write_d<E, 128>(a, s);
+  return launch_write_d<E, 256>(a, s);
 }
 
 }  // namespace

@@ -680,8 +680,8 @@ def paged_plan(lens, add, table, free_list, free_pos, page, rows, lens_out=None,
                  ("free_pos_out", free_pos_out, i64, (2,)))
     on = _On(dev, stream)
     if out is None:
-        cu, page_cu, slot, row_req, row_len, status, new = on.empty(
-            (4 * B + 2 + 3 * rows,), i32).split((B + 1, B + 1, rows, rows, rows, B, B))
+        cu, page_cu, slot, row_req, row_len, status, new = torch.split_with_sizes(
+            on.empty((4 * B + 2 + 3 * rows,), i32), (B + 1, B + 1, rows, rows, rows, B, B))
         out = dict(cu=cu, page_cu=page_cu, slot=slot, row_req=row_req, row_len=row_len,
                    status=status, lens=new if lens_out is None else lens_out,
                    free_pos=on.empty((2,), i64) if free_pos_out is None else free_pos_out)
