@@ -77,7 +77,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
   constexpr int NS = D / 32;                     // reduction steps of the scores
   constexpr int EPL = D / 16;                    // elements of V per lane and key
   constexpr int DW = EPL * (int)sizeof(E) / 4;   // the same in words
-  constexpr bool TWO = sizeof(E) == 2 && sizeof(O) == 4;   // weights in two parts
+  constexpr bool TWO = sizeof(E) == 2;           // weights in two parts
   constexpr float BIAS = Bias<E>::V;
   constexpr int LD = D + 4;                      // LDS row: the pad spreads heads over banks
   __shared__ float joined[NW][16][LD];

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
   constexpr int BUF = 2 * SK * D;      // elements of a stage: K, then V
   constexpr int RU = D / 8;            // 16-byte units of a row
   constexpr int NU = SK * 2 * RU / NT; // of a stage, for a thread
-  constexpr bool TWO = sizeof(O) == 4;
+  constexpr bool TWO = sizeof(O) == 4;  // weights in two parts
   constexpr float BIAS = sizeof(E) == 2 && __is_same(E, fp16) ? 10.f : 0.f;   // see paged_attend.hip
   extern __shared__ __attribute__((aligned(16))) char lds[];
   E* stage = reinterpret_cast<E*>(lds);
