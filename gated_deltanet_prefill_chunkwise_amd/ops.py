@@ -8,6 +8,7 @@ stream).  The library is loaded on first use; a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -592,7 +593,9 @@ def _row_view(t, name, device, dtype, shape):
     return ld if rows > 1 else heads * d
 
 
+@functools.lru_cache(maxsize=256)
 def _paged(rows, q_heads, cache_shape, dtype, out_dtype=None, batch=1, width=1, max_len=None):
+    """The shape of a call, by its sizes (made once for each: small calls are bound by this side)."""
     n_pages, n_kv, page, d = cache_shape
     code = _ocode(dtype)
     return Paged(rows, batch, q_heads, n_kv, d, page, n_pages, width,
@@ -605,9 +608,14 @@ def paged_workspace_bytes(shape: Paged, n_blocks=0, select=False) -> int:
     return int(lib().sgdn_paged_workspace_bytes(ctypes.byref(shape), int(n_blocks), int(select)))
 
 
-def _paged_ws(shape, n_blocks, select, on, workspace):
-    """(pointer, bytes, tensor) of the call's workspace."""
-    nbytes = paged_workspace_bytes(shape, n_blocks, select)
+@functools.lru_cache(maxsize=256)
+def _paged_bytes(n_blocks, select, *sizes):
+    return paged_workspace_bytes(_paged(*sizes), n_blocks, select)
+
+
+def _paged_ws(n_blocks, select, on, workspace, *sizes):
+    """(pointer, bytes, tensor) of the call's workspace; ``sizes`` as for _paged."""
+    nbytes = _paged_bytes(n_blocks, select, *sizes)
     if nbytes == 0:
         raise SgdnError(-2, "sgdn_paged_workspace_bytes")
     import torch
@@ -758,9 +766,10 @@ def _attend(name, q, k_cache, v_cache, table, row_len, row_req, blocks, scale, m
                  ("row_req", row_req, i32, (rows,)),
                  ("blocks", blocks, i32, (rows, n_kv, n_blocks)),
                  ("o", o, None, (rows, n_q, d)), ("lse", lse, torch.float32, (rows, n_q)))
-    shape = _paged(rows, n_q, k_cache.shape, dt, out_dtype, B, W, max_len)
+    sizes = (rows, n_q, k_cache.shape, dt, out_dtype, B, W, max_len)
+    shape = _paged(*sizes)
     on = _On(dev, stream)
-    ws, nbytes, held = _paged_ws(shape, n_blocks, False, on, workspace)
+    ws, nbytes, held = _paged_ws(n_blocks, False, on, workspace, *sizes)
     if o is None:
         o = on.empty((rows, n_q, d), out_dtype)
     if want_lse and lse is None:
@@ -821,9 +830,10 @@ def paged_select(q, codes, code_scale, table, row_len, page, n_blocks, row_req=N
                  ("table", table, i32, None), ("row_len", row_len, i32, (rows,)),
                  ("row_req", row_req, i32, (rows,)),
                  ("blocks", blocks, i32, (rows, n_kv, n_blocks)))
-    shape = _paged(rows, q.shape[1], (n_pages, n_kv, page, d), q.dtype, None, B, W, max_len)
+    sizes = (rows, q.shape[1], (n_pages, n_kv, page, d), q.dtype, None, B, W, max_len)
+    shape = _paged(*sizes)
     on = _On(dev, stream)
-    ws, nbytes, held = _paged_ws(shape, n_blocks, True, on, workspace)
+    ws, nbytes, held = _paged_ws(n_blocks, True, on, workspace, *sizes)
     if blocks is None:
         blocks = on.empty((rows, n_kv, n_blocks), i32)
     on.call("sgdn_paged_select", ctypes.byref(shape), q.data_ptr(), ldq, codes.data_ptr(),
