@@ -91,7 +91,7 @@ hipError_t launch_paged_write(const PageWriteArgs& a, int dtype, int d, hipStrea
 int paged_splits(long long units, int tiles, int row_bytes);
 hipError_t launch_paged_attend(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 // Rows of a tile of launch_paged_tiles, 0 where it is not used.
-int paged_tile_rows(int R, int B, int G, int Hkv, bool has_req, int dtype, int lp, int max_len, int n_blocks);
+int paged_tile_rows(int R, int B, int G, int Hkv, int d, bool has_req, int dtype, int lp, int max_len, int n_blocks);
 hipError_t launch_paged_tiles(const PageAttendArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 hipError_t launch_paged_select(const PageSelectArgs& a, int dtype, int d, hipStream_t s);
 

@@ -78,7 +78,7 @@ AttendPlan attend_plan(const sgdn_paged* p, int n_blocks, bool has_req) {
   }
   pl.TQ = 0;
   if (n_blocks > 0 && pl.S == 1 && p->rows > 0)
-    pl.TQ = paged_tile_rows(p->rows, p->batch, G, p->n_kv, has_req, p->dtype, log2_page(p->page), longest(p), n_blocks);
+    pl.TQ = paged_tile_rows(p->rows, p->batch, G, p->n_kv, p->d, has_req, p->dtype, log2_page(p->page), longest(p), n_blocks);
   if (pl.TQ > 0)
     pl.total = NO_WORKSPACE + align256((size_t)((p->rows + pl.TQ - 1) / pl.TQ) * p->n_kv * sizeof(int32_t));
   if (pl.total == 0) pl.total = NO_WORKSPACE;

@@ -381,9 +381,13 @@ template <typename E> hipError_t launch_e(const PageAttendArgs& a, int o_dtype, 
 }  // namespace
 
 // Splits of each unit's keys: `groups` workgroups to keep every CU's memory
-// pipeline busy, but a tile at least for each wave of one.
+// pipeline busy, but a tile at least for each wave of one.  More groups mean
+// more to join: with rows of 512 bytes 256 groups take 48 and 102 us and 512
+// take 51 and 105 (1 and 2 sequences of 131072, 2 heads of 256, fp16); with
+// shorter rows 512 take 16.9 and 256 17.7 (4 of 4096, 8 heads of 128, bf16;
+// 1024: 19.0), 20.0 and 20.8 (7 of 5001, 3 heads of 64, fp32; 1024: 19.7).
 int paged_splits(long long units, int tiles, int row_bytes) {
-  const int groups = row_bytes >= 512 ? 512 : 1024;
+  const int groups = row_bytes >= 512 ? 256 : 512;
   const long long want = (groups + units - 1) / units;
   const long long most = (tiles + NW - 1) / NW;
   const long long s = want < most ? want : most;

@@ -474,9 +474,13 @@ __global__ __launch_bounds__(NWV == 1 ? 256 : 64 * NWV) void pick_kernel(PageSel
 }
 
 template <typename E, int D> hipError_t launch_score_d(const PageSelectArgs& a, hipStream_t s) {
-  // More rows than requests: some request has several rows, which can share
-  // its pages.  Otherwise (or with more heads than a tile) a row at a time.
-  if (a.R > a.B && a.G <= 16) {
+  // Several rows of a request share its pages, if there are enough of them to
+  // fill the chip; otherwise (or with more heads than a tile) a row at a time.
+  // Shared and alone, 512 blocks, 32/8 heads of 128: 32 requests with 2, 4, 8
+  // and 32 rows each 41 and 19, 33 and 29, 29 and 39, 42 and 119 us; 256 with 4
+  // each 61 and 119; 1 request with 16, 64, 128 rows 16 and 12, 19 and 18, 21
+  // and 26; 16/2 heads of 256: 16 with 16 each (1000 blocks) 26 and 35.
+  if (a.R >= 4 * (int64_t)a.B && (int64_t)a.R * a.Hkv * D >= 1 << 17 && a.G <= 16) {
     int gp = 1;
     while (gp < a.G) gp <<= 1;
     const unsigned per = tiles_of_wave(gp) * SW * (16 / gp), gx = (a.R + per - 1) / per;
@@ -514,12 +518,14 @@ hipError_t launch_paged_select(const PageSelectArgs& a, int dtype, int d, hipStr
     e = dtype == 1 ? launch_score<bf16>(a, d, s) : dtype == 2 ? launch_score<fp16>(a, d, s) : launch_score<float>(a, d, s);
   if (e != hipSuccess) return e;
   // One wave for each row while it holds the scores in 4 registers, or in 16
-  // where the rows alone fill the chip; else as many waves as that takes.
+  // where the rows alone fill the chip (1000 blocks, scores included: 2048 rows
+  // 66.9 us with one wave and 68.3 with four, 256 rows 21.2 and 18.6); else as
+  // many waves as that takes.
   const long long rows = (long long)a.R * a.Hkv;
   const dim3 many((unsigned)rows), four((unsigned)((rows + 3) / 4));
   if (a.NB <= 64) hipLaunchKernelGGL((pick_kernel<1, 1>), four, dim3(256), 0, s, a);
   else if (a.NB <= 256) hipLaunchKernelGGL((pick_kernel<1, 4>), four, dim3(256), 0, s, a);
-  else if (a.NB <= 1024 && rows >= 4096) hipLaunchKernelGGL((pick_kernel<1, 16>), four, dim3(256), 0, s, a);
+  else if (a.NB <= 1024 && rows >= 2048) hipLaunchKernelGGL((pick_kernel<1, 16>), four, dim3(256), 0, s, a);
   else if (a.NB <= 1024) hipLaunchKernelGGL((pick_kernel<4, 4>), many, dim3(256), 0, s, a);
   else if (a.NB <= 2048) hipLaunchKernelGGL((pick_kernel<4, 8>), many, dim3(256), 0, s, a);
   else if (a.NB <= 4096) hipLaunchKernelGGL((pick_kernel<4, 16>), many, dim3(256), 0, s, a);

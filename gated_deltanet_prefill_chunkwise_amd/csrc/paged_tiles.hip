@@ -4,8 +4,7 @@
 // head, walks the union of its rows' lists once and lets each column use the
 // blocks that its row listed.  Where 16 rows list 16 blocks each and share
 // most, a block is fetched once instead of a dozen times.  Rows that share
-// little are better off alone: a tile whose union has more than SPARSE_UNION
-// blocks for each block of a row is left to the kernel for single rows.
+// little are better off alone: such a tile is left to the kernel for single rows.
 //
 // A wave owns 32 columns (16 at D = 256); both products run transposed with
 // 16 x 16 x 32 matrix instructions as in paged_attend.hip.  Keys and values come in stages of 32
@@ -34,7 +33,17 @@ constexpr int SK = 32;                 // keys of a stage
 // 256 elements their accumulators do not fit the registers.
 constexpr int tiles_of_wave(int d) { return d == 256 ? 1 : 2; }
 
-constexpr int SPARSE_UNION = 4;
+// What is left alone.  A block of the union costs a tile as much as GAIN
+// blocks of single rows' lists cost the kernel for these while the chip is
+// full; with fewer than `full` tiles the tiles still take as long as `full`
+// would, as a tile walks its union alone.  Tiles and single rows, 4096 rows of
+// 16 of 256 blocks of 64 keys, where 32, 4, 2 or 1 neighbouring rows have one
+// list: 32/8 heads of 128 172, 720, 1123, 1506 and 1148 to 1184 us; 16/2 of 256
+// (1024 rows: 76 and 158) 391, 653, 1075 for 4, 2, 1 and 595 to 695; 16/1 of 128
+// 77, 122, 192, 358 and 158 to 164; 8/8 of 64 163, 428 (8 alike), 612 (1) and 683.  256
+// rows that are all alike: 58 and 78 (32/8 of 128), 69 and 46 (16/2 of 256).
+constexpr int GAIN = 3;
+constexpr int full_of(int d) { return d == 256 ? 256 : 512; }
 constexpr int LIST = 256;              // blocks of the union that are listed at a time (8 words of bits)
 
 // Position of 16-byte unit c of row `key`.  An access reads the keys whose bit 2
@@ -63,7 +72,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
   uint32_t* rowbits = reinterpret_cast<uint32_t*>(lds + 2 * BUF * sizeof(E));   // [TQ][words]
   uint32_t* uni = rowbits + TQ * words;                                          // [words]
   __shared__ int row_len[COLS];
-  __shared__ int req_max, req_min, len_max, more, bad, n_list, n_entries, n_rows;
+  __shared__ int req_max, req_min, len_max, more, bad, n_list, n_entries;
   __shared__ int2 list[LIST];
 
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -75,7 +84,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
   const int h = unit / tiles, tile = unit - h * tiles, row0 = tile * TQ;
   int32_t* done = a.done + (size_t)tile * a.Hkv + h;
 
-  if (tid == 0) { req_max = -1; req_min = 0x7fffffff; len_max = 0; bad = 0; n_entries = 0; n_rows = 0; }
+  if (tid == 0) { req_max = -1; req_min = 0x7fffffff; len_max = 0; bad = 0; n_entries = 0; }
   lds_barrier();
   if (tid < TQ) {
     const int r = row0 + tid;
@@ -86,7 +95,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
     }
     if (req < 0 || req >= a.B || len <= 0) len = 0;
     row_len[tid] = len;
-    if (len > 0) { atomicMax(&req_max, req); atomicMin(&req_min, req); atomicMax(&len_max, len); atomicAdd(&n_rows, 1); }
+    if (len > 0) { atomicMax(&req_max, req); atomicMin(&req_min, req); atomicMax(&len_max, len); }
   }
   lds_barrier();
   const int req = __builtin_amdgcn_readfirstlane(req_max);
@@ -171,7 +180,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
       for (int i = lane; i < nw; i += 64) blocks += __builtin_popcount(uni[i]);
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) blocks += __shfl_xor(blocks, o, 64);
-      if ((int64_t)__builtin_amdgcn_readfirstlane(blocks) * n_rows > SPARSE_UNION * (int64_t)n_entries) {
+      if (GAIN * (int64_t)__builtin_amdgcn_readfirstlane(blocks) * max(units, full_of(D)) > (int64_t)units * n_entries) {
         if (tid == 0) *done = 0;
         return;
       }
@@ -425,16 +434,16 @@ template <typename E> hipError_t launch_o(const PageAttendArgs& a, int o_dtype, 
 }  // namespace
 
 // Rows of a tile, or 0 where the tiles do not serve: 32-bit types, more heads
-// than columns of a tile's row share, no or few rows of a request each, too
-// few tiles for the chip, lists and contexts beyond the tile's tables in LDS.
-int paged_tile_rows(int R, int B, int G, int Hkv, bool has_req, int dtype, int lp, int max_len, int n_blocks) {
+// than columns of a tile's row share, no or few rows of a request each, so few
+// that tiles lose even if all rows have one list, lists and contexts beyond the
+// tile's tables in LDS.
+int paged_tile_rows(int R, int B, int G, int Hkv, int d, bool has_req, int dtype, int lp, int max_len, int n_blocks) {
   if (dtype == 0 || G > 16 || !has_req || R < 4 * (long long)B) return 0;
   int gp = 1;
   while (gp < G) gp <<= 1;
   const int tq = COLS / gp;
-  const long long tiles = ((long long)R + tq - 1) / tq;
   const long long words = ((((long long)max_len - 1) >> lp) >> 5) + 1;
-  if (tiles * Hkv < 128 || (long long)tq * n_blocks > 32 * 256 || (tq + 1) * words * 4 > 15 * 1024) return 0;
+  if ((long long)R * Hkv < GAIN * full_of(d) || (long long)tq * n_blocks > 32 * 256 || (tq + 1) * words * 4 > 15 * 1024) return 0;
   return tq;
 }
 

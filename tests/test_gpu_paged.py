@@ -397,6 +397,29 @@ def test_select_rows_of_requests(Hq, Hkv):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Hq, Hkv, D", [(2, 2, 64), (4, 2, 256), (8, 2, 128), (6, 2, 64), (16, 2, 128), (16, 1, 256), (24, 1, 128)])
+def test_select_many_rows_of_requests(Hq, Hkv, D, dtype):
+    """So many rows that those of a request share its pages, across the borders of requests."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    rng = np.random.default_rng(Hq + D)
+    P, W, B = 16, 21, 6
+    codes, scale, dc, ds = _summaries(rng, B * W, Hkv, D)
+    table = rng.permutation(B * W).reshape(B, W).astype(np.int32)
+    table[2, 5], table[3, 2] = -1, B * W
+    n = (1 << 17) // (Hkv * D) + 60
+    req = np.r_[[5] * 7, [1] * (n // 3), [3, 0, 3, 9, 3], [-1], [2] * (n - n // 3), [4] * 2, [-1] * 3].astype(np.int32)
+    length = rng.integers(1, W * P + 1, len(req)).astype(np.int32)
+    length[-3:], length[40:42] = 0, (-1, 0)
+    q = torch.from_numpy(rng.standard_normal((len(req), Hq, D))).cuda().to(_t(dtype))
+    for K, max_len in ((6, None), (16, 300)):
+        got = ops.paged_select(q, dc, ds, _i32(table), _i32(length), P, K, row_req=_i32(req), max_len=max_len)
+        torch.cuda.synchronize()
+        want = ref.select(_f64(q), codes, scale, table, length, P, K, req=req, max_len=max_len)
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_select_values_that_are_not_finite():
     import torch
     from gated_deltanet_prefill_chunkwise_amd import ops
@@ -627,13 +650,15 @@ def test_attend_sparse_prompts(Hq, Hkv, D, P, K, dtype, out):
     from gated_deltanet_prefill_chunkwise_amd import ops
     G = Hq // Hkv
     gp = 1 << (G - 1).bit_length()
-    R = 128 * (128 // gp) // Hkv + 50              # as many tiles as it takes
+    R = 256 * (128 // gp) // Hkv + 50              # as many tiles as it takes
     new = [R - R // 3, R // 3 - 1, 1]
     lens = np.array(new) + [70, 3, 200]
-    c, req, length, lists, q = _prompt(Hq + D + P, Hq, Hkv, D, P, dtype, K, lens, new)
+    c, req, length, lists, q = _prompt(Hq + D + P, Hq, Hkv, D, P, dtype, K, lens, new, alike=16)
     t = [_i32(x) for x in (c.table, length, lists, req)]
-    o, lse = ops.paged_attend_sparse(q, c.k, c.v, t[0], t[1], t[2], row_req=t[3], out_dtype=_t(out), want_lse=True)
+    ws = torch.full((1 << 16,), 7, dtype=torch.uint8, device="cuda")
+    o, lse = ops.paged_attend_sparse(q, c.k, c.v, t[0], t[1], t[2], row_req=t[3], out_dtype=_t(out), want_lse=True, workspace=ws)
     torch.cuda.synchronize()
+    assert (ws.view(torch.int32) == 1).sum() >= 40, "tiles, and not single rows alone"
     rows = np.unique(np.r_[np.arange(0, 40), c.rng.integers(0, len(req), 60), new[0] - 20 + np.arange(40), len(req) - 30 + np.arange(30)])
     want = ref.attend(_f64(q[rows]), _f64(c.k), _f64(c.v), c.table, length[rows], req[rows], blocks=lists[rows])
     i = torch.from_numpy(rows).cuda()
@@ -645,8 +670,8 @@ def test_attend_scale(scale):
     """Scales of either sign and 0, for single rows and for tiles of rows."""
     import torch
     from gated_deltanet_prefill_chunkwise_amd import ops
-    R = 128 * 16 + 9
-    c, req, length, lists, q = _prompt(9, 8, 1, 64, 32, "bf16", 3, np.array([R + 60]), [R], pad=0)
+    R = 256 * 16 + 9
+    c, req, length, lists, q = _prompt(9, 8, 1, 64, 32, "bf16", 3, np.array([R + 60]), [R], pad=0, alike=16)
     t = [_i32(x) for x in (c.table, length, lists, req)]
     rows = np.arange(0, R, 57)
     i = torch.from_numpy(rows).cuda()
@@ -659,24 +684,30 @@ def test_attend_scale(scale):
         check(o[j], lse[j], want, "f32", "bf16", 64)
 
 
-def test_attend_sparse_prompts_see_only_their_own():
+@pytest.mark.parametrize("alike", [1, 16])
+def test_attend_sparse_prompts_see_only_their_own(alike):
     """A row's result does not change with what other rows of its tile list or see: values
     that are not finite in their blocks, in later tokens, or an infinite score of one."""
     import torch
     from gated_deltanet_prefill_chunkwise_amd import ops
-    R = 128 * 16 + 9
-    c, req, length, lists, q = _prompt(5, 8, 1, 64, 16, "bf16", 4, np.array([R + 60]), [R], pad=0, alike=1)
+    R = 256 * 16 + 9
+    c, req, length, lists, q = _prompt(5, 8, 1, 64, 16, "bf16", 4, np.array([R + 60]), [R], pad=0, alike=alike)
     t = [_i32(x) for x in (c.table, length, lists, req)]
-    call = lambda: ops.paged_attend_sparse(q, c.k, c.v, t[0], t[1], t[2], row_req=t[3], want_lse=True)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    call = lambda: ops.paged_attend_sparse(q, c.k, c.v, t[0], t[1], t[2], row_req=t[3], want_lse=True, workspace=ws)
     o, lse = call()
+    assert ((ws.view(torch.int32) == 1).sum() >= 100) == (alike > 1)     # tiles, or single rows alone
     bad = c.table[0, [3, 40, 100]]
     c.v[bad[0], 0, 5, 7], c.v[bad[1], 0, 2] = float("nan"), float("inf")
     c.k[bad[2], 0, 9, 3] = float("inf")
     o2, lse2 = call()
     torch.cuda.synchronize()
-    hit = np.zeros(R, bool)
+    hit, spoilt = np.zeros(R, bool), np.zeros(R, bool)
+    above = (_f64(q)[:, :, 3] > 0).any(-1)       # else the infinite key's scores are -inf, which weigh 0
     for j, place in ((3, 5), (40, 2), (100, 9)):
-        hit |= (lists[:, 0] == j).any(-1) & (length > 16 * j + place)
+        one = (lists[:, 0] == j).any(-1) & (length > 16 * j + place)
+        hit |= one
+        spoilt |= one & (above if j == 100 else True)
     assert 0 < hit.sum() < R
     clean = torch.from_numpy(~hit).cuda()
     # the kernel for single rows sums in another order than the tiles: equal within both bounds
@@ -686,4 +717,4 @@ def test_attend_sparse_prompts_see_only_their_own():
     check(o2[i], lse2[i], want, "f32", "bf16", 64)
     check(o[i], lse[i], want, "f32", "bf16", 64)
     assert torch.isfinite(o2[clean]).all() and torch.isfinite(o).all()
-    assert not torch.isfinite(o2[~clean].reshape(int(hit.sum()), -1)).all(-1).any()
+    assert not torch.isfinite(o2[torch.from_numpy(spoilt).cuda()].reshape(int(spoilt.sum()), -1)).all(-1).any()

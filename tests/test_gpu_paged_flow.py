@@ -151,7 +151,7 @@ def test_captured_step_replays():
         torch.ones(1 << 20, device="cuda").sum().item()
 
 
-def _prompt_call(seed, rows=2200):
+def _prompt_call(seed, rows=4200):
     import torch
     rng = np.random.default_rng(seed)
     n = rows + 50
