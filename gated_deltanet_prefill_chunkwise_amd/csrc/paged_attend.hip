@@ -38,6 +38,7 @@ namespace {
 constexpr int NW = 4;        // waves of a workgroup
 constexpr int KT = 32;       // keys of a tile
 constexpr int MAX_SPLITS = 256;
+constexpr unsigned LEFT_GRID = 2048;   // of the rows that tiles left
 
 template <typename E> struct Bias { static constexpr float V = 0.f; };
 template <> struct Bias<fp16> { static constexpr float V = 10.f; };
@@ -72,32 +73,28 @@ template <typename E> __device__ __forceinline__ frag_t<E> ld8a(const E* p) {   
 // many of them take part.
 struct Half { size_t row; int n; };
 
-template <typename E, typename O, int D, bool SPARSE>
-__global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel(PageAttendArgs a, int units) {
+template <int D> struct Joined {
+  float o[NW][16][D + 4];      // the pad spreads heads over banks
+  float ml[NW][16][2];
+};
+
+// One split of one (head tile, row, key/value head).
+template <typename E, typename O, int D, bool SPARSE, bool LOOP>
+__device__ __forceinline__ void attend_unit(const PageAttendArgs& a, int unit, int split, Joined<D>& lds) {
   constexpr int NS = D / 32;                     // reduction steps of the scores
   constexpr int EPL = D / 16;                    // elements of V per lane and key
   constexpr int DW = EPL * (int)sizeof(E) / 4;   // the same in words
   constexpr bool TWO = sizeof(E) == 2;           // weights in two parts
   constexpr float BIAS = Bias<E>::V;
-  constexpr int LD = D + 4;                      // LDS row: the pad spreads heads over banks
-  __shared__ float joined[NW][16][LD];
-  __shared__ float ml[NW][16][2];
+  auto& joined = lds.o;
+  auto& ml = lds.ml;
 
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (LOOP) asm volatile("" : "+v"(lane), "+s"(wave));   // keep nothing made of them from unit to unit
   const int n = lane & 15, g = lane >> 4;
-  int unit = blockIdx.x / a.S;
-  const int split = blockIdx.x - unit * a.S;
-  // Rows next to each other (SPARSE) and the head tiles of a group read the
-  // same pages: give each XCD (workgroup id mod 8) one run of them.
-  if (SPARSE || a.MT > 1) {
-    const int per = (units + 7) >> 3;
-    unit = (unit & 7) * per + (unit >> 3);
-    if (unit >= units) return;
-  }
   const int mt = unit % a.MT;
   const int rh = unit / a.MT;
   const int h = rh / a.R, row = rh - h * a.R;
-  if (SPARSE && a.done != nullptr && a.done[(size_t)(row / a.TQ) * a.Hkv + h] != 0) return;   // made with its tile
   const int req = a.row_req == nullptr ? row : a.row_req[row];
   const int P = 1 << a.lp;
   int len = min(a.row_len[row], a.max_len);
@@ -295,6 +292,46 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
   }
 }
 
+// Rows next to each other (SPARSE) and the head tiles of a group read the same
+// pages: each XCD (workgroup id mod 8) gets one run of the units.
+__device__ __forceinline__ int unit_of_xcd(int i, int units) { return (i & 7) * ((units + 7) >> 3) + (i >> 3); }
+
+template <typename E, typename O, int D, bool SPARSE>
+__global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel(PageAttendArgs a, int units) {
+  __shared__ Joined<D> lds;
+  int unit = blockIdx.x / a.S;
+  const int split = blockIdx.x - unit * a.S;
+  if (SPARSE || a.MT > 1) {
+    unit = unit_of_xcd(unit, units);
+    if (unit >= units) return;
+  }
+  attend_unit<E, O, D, SPARSE, false>(a, unit, split, lds);
+}
+
+// The rows that the tiles left, S = MT = 1.  Most often there are none, and a
+// workgroup for each row takes 28 us to find that out (8192 rows and heads);
+// so 2048 workgroups look 64 of their units up at a time.  Whole calls of 4096
+// rows of 16 of 256 blocks, a workgroup a row and so: 171 and 146 us (32/8 heads
+// of 128, nothing left), 160 and 155 (16/2 of 256); 1208 and 1275, 715 and 764
+// where every row is left, as the work is dealt out ahead.
+template <typename E, typename O, int D>
+__global__ __launch_bounds__(64 * NW, 2) void left_kernel(PageAttendArgs a, int units) {
+  __shared__ Joined<D> lds;
+  const int all = (units + 7) / 8 * 8;                   // a multiple of 8, like the grid
+  for (int64_t first = blockIdx.x; first < all; first += 64 * (int64_t)gridDim.x) {
+    const int64_t at = first + lane_id() * (int64_t)gridDim.x;
+    const int u = unit_of_xcd((int)min(at, (int64_t)all - 1), units);
+    const int h = min(u, units - 1) / a.R, row = min(u, units - 1) - h * a.R;
+    uint64_t left = __ballot(at < all && u < units && a.done[(size_t)(row / a.TQ) * a.Hkv + h] == 0);
+    while (left != 0) {
+      const int i = __builtin_ctzll(left);
+      left &= left - 1;
+      attend_unit<E, O, D, true, true>(a, unit_of_xcd((int)(first + i * (int64_t)gridDim.x), units), 0, lds);
+      __syncthreads();                                   // before the next unit writes lds
+    }
+  }
+}
+
 // Joins the S <= 256 splits of 64 elements of a (row, query head): thread t
 // sums elements 4 (t % 16) .. of the splits t / 16 + 16 i.
 template <typename O, int D>
@@ -356,6 +393,12 @@ __global__ __launch_bounds__(256) void join_kernel(PageAttendArgs a) {
 template <typename E, typename O, int D> hipError_t launch_d(const PageAttendArgs& a, hipStream_t s) {
   const int units = a.R * a.Hkv * a.MT;
   const unsigned grid = (unsigned)((a.blocks != nullptr || a.MT > 1 ? (units + 7) / 8 * 8 : units) * a.S);
+  if constexpr (sizeof(E) == 2) {
+    if (a.done != nullptr) {
+      hipLaunchKernelGGL((left_kernel<E, O, D>), dim3(grid < LEFT_GRID ? grid : LEFT_GRID), dim3(64 * NW), 0, s, a, units);
+      return hipGetLastError();
+    }
+  }
   if (a.blocks != nullptr)
     hipLaunchKernelGGL((attend_kernel<E, O, D, true>), dim3(grid), dim3(64 * NW), 0, s, a, units);
   else
