@@ -20,6 +20,15 @@
 // A tile whose result is not finite anywhere, or whose rows belong to
 // different requests, is left (done = 0) as well: that kernel runs behind and
 // reads for each row its own blocks only.
+//
+// Bound: the steps of a stage, which follow each other: 272 us for 4096 rows
+// of 16 of 256 blocks of 64 keys in four requests (16/2 heads of 256, bf16);
+// without the products or the exponentials 261, without the copies 215, without
+// the copies and the LDS reads 173.  (Their least is 41 us of products if each
+// row had only its own.)  Tried at those sizes and slower: 32 x 32 x 16
+// instructions (300), 64 columns a workgroup (285), all of K's LDS reads at once
+// (292), copies straight to LDS (395); 64-key stages of wave pairs that share
+// weights: 243, but 147 and not 118 at D = 128.
 #include "common.h"
 #include "paged.h"
 
@@ -65,7 +74,10 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
   constexpr int BUF = 2 * SK * D;      // elements of a stage: K, then V
   constexpr int RU = D / 8;            // 16-byte units of a row
   constexpr int NU = SK * 2 * RU / NT; // of a stage, for a thread
-  constexpr bool TWO = sizeof(O) == 4;  // weights in two parts
+  // Weights in two parts, as in paged_attend.hip, cost the matrix cores half as
+  // much again.  A 16-bit o errs by half a step of its type in any case, and
+  // weights rounded once add no more than that of the weighted mean of |v|.
+  constexpr bool TWO = sizeof(O) == 4;
   constexpr float BIAS = sizeof(E) == 2 && __is_same(E, fp16) ? 10.f : 0.f;   // see paged_attend.hip
   extern __shared__ __attribute__((aligned(16))) char lds[];
   E* stage = reinterpret_cast<E*>(lds);

@@ -41,9 +41,11 @@
  * - Types: q, k, v and the caches share one of fp32, bf16, fp16; o is any of
  *   them.  Products run on the matrix cores with fp32 accumulation; the
  *   softmax maximum, sum and the output accumulate in fp32.  With 16-bit
- *   inputs the softmax weights enter their product rounded to that type (an
- *   fp32 o takes them as two 16-bit parts, so that o has fp32's accuracy);
- *   with fp32 inputs nothing is rounded below fp32.
+ *   inputs the softmax weights enter their product as two numbers of that type
+ *   (weight and remainder), so that o errs by fp32's rounding and its own; only
+ *   rows that share their lists (sgdn_paged_attend_sparse of many rows, 16-bit
+ *   o) take weights rounded once to the type, half the products.  With fp32
+ *   inputs nothing is rounded below fp32.
  * - Alignment: q, k, v, the caches, codes and o start at 16 bytes; row
  *   strides are multiples of 16 bytes.  Otherwise SGDN_EINVAL.
  */
