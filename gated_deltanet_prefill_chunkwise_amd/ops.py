@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -524,10 +525,10 @@ class _On:
         self.device = device
         self.away = index != torch._C._cuda_getDevice()
         self.raw = torch._C._cuda_getCurrentRawStream(index)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         self.other = stream is not None and stream.cuda_stream != self.raw
         if self.other:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
             self.stream = stream
             self.raw = stream.cuda_stream
 
@@ -597,9 +598,11 @@ def _row_view(t, name, device, dtype, shape):
 def _paged(rows, q_heads, cache_shape, dtype, out_dtype=None, batch=1, width=1, max_len=None):
     """The shape of a call, by its sizes (made once for each: small calls are bound by this side)."""
     n_pages, n_kv, page, d = cache_shape
+    if max_len is not None and max_len < 1:
+        raise ValueError(f"max_len must be positive (or None), got {max_len}")
     code = _ocode(dtype)
     return Paged(rows, batch, q_heads, n_kv, d, page, n_pages, width,
-                 0 if max_len is None else int(max_len), code,
+                 0 if max_len is None else max_len, code,
                  code if out_dtype is None else _ocode(out_dtype))
 
 
@@ -750,6 +753,7 @@ def _attend(name, q, k_cache, v_cache, table, row_len, row_req, blocks, scale, m
     ldq = _row_view(q, "q", dev, dt, (None, None, d))
     rows, n_q, _ = q.shape
     B, W = _table_shape(table)
+    max_len = None if max_len is None else operator.index(max_len)   # a key below: no tensor
     n_blocks, lists = 0, ()
     if blocks is not None:
         if blocks.dim() != 3 or blocks.shape[2] < 1:
@@ -823,6 +827,8 @@ def paged_select(q, codes, code_scale, table, row_len, page, n_blocks, row_req=N
     ldq = _row_view(q, "q", dev, q.dtype, (None, None, d))
     rows = q.shape[0]
     B, W = _table_shape(table)
+    page, n_blocks = operator.index(page), operator.index(n_blocks)
+    max_len = None if max_len is None else operator.index(max_len)
     if row_req is None and rows > B:
         raise ValueError("without row_req, row r is request r: more rows than requests")
     _paged_check(dev, ("codes", codes, torch.int8, None),

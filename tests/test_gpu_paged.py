@@ -616,6 +616,27 @@ def test_binding_refusals():
     torch.cuda.synchronize()
 
 
+def test_max_len_as_given():
+    """An upper bound that is a tensor counts with its value at the call; 0 is none."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    c = Case(83, [20, 60], 4, 2, 64, 16, "f32")
+    t, n, q = _i32(c.table), _i32(c.lens), c.q(2)
+    codes, _, dc, ds = _summaries(c.rng, len(c.k), 2, 64)
+    most = torch.tensor(60)
+    for m in (60, 33, 1):
+        most.fill_(m)
+        o, lse = ops.paged_attend(q, c.k, c.v, t, n, max_len=most, want_lse=True)
+        got = ops.paged_select(q, dc, ds, t, n, torch.tensor(16), 2, max_len=most)
+        torch.cuda.synchronize()
+        want = ref.attend(_f64(q), _f64(c.k), _f64(c.v), c.table, np.minimum(c.lens, m), np.arange(2))
+        check(o, lse, want, "f32", "f32", 64)
+        assert np.array_equal(got.cpu().numpy(), ref.select(_f64(q), codes, _f64(ds).astype(np.float32), c.table, c.lens, 16, 2, max_len=m))
+    for m in (0, -5, 61.0):
+        with pytest.raises((ValueError, TypeError)):
+            ops.paged_attend(q, c.k, c.v, t, n, max_len=m)
+
+
 # attend_sparse of prompts ----------------------------------------------------
 
 
