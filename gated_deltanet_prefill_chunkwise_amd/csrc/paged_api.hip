@@ -42,7 +42,7 @@ int check_shape(const sgdn_paged* p) {
   if (log2_page(p->page) < 0) return SGDN_EUNSUPPORTED;
   if (p->n_q % p->n_kv != 0) return SGDN_EUNSUPPORTED;
   if (p->n_kv > 65535) return SGDN_EUNSUPPORTED;                     // a grid dimension
-  if ((int64_t)p->rows * p->n_q > (INT64_C(1) << 28)) return SGDN_EUNSUPPORTED;
+  if ((int64_t)p->rows * p->n_q >= (INT64_C(1) << 28)) return SGDN_EUNSUPPORTED;
   if ((int64_t)p->n_pages * p->page >= (INT64_C(1) << 31)) return SGDN_EUNSUPPORTED;
   return SGDN_OK;
 }
@@ -57,7 +57,19 @@ int check_read(const sgdn_paged* p) {
   return SGDN_OK;
 }
 
+// A launch holds fewer than 2^32 threads: `groups` workgroups, in eighths of
+// the chip, of `threads`.
+bool too_many(int64_t groups, int threads) { return (groups + 7) / 8 * 8 * threads >= (INT64_C(1) << 32); }
+
+// Rows, heads and head tiles of the attention: a workgroup of 256 each.
+bool too_many_units(const sgdn_paged* p) {
+  return too_many((int64_t)p->rows * p->n_kv * ((p->n_q / p->n_kv + 15) / 16), 256);
+}
+
 int longest(const sgdn_paged* p) { return p->max_len > 0 ? p->max_len : p->width * p->page; }
+
+// Rows and heads of the choice: a workgroup of up to 1024 each.
+bool too_many_picks(const sgdn_paged* p) { return too_many((int64_t)p->rows * p->n_kv, 1024); }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -98,7 +110,8 @@ int attend(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache,
   const int st = check_read(p);
   if (st != SGDN_OK) return st;
   if (p->o_dtype != SGDN_F32 && p->o_dtype != SGDN_BF16 && p->o_dtype != SGDN_F16) return SGDN_EINVAL;
-  if (!isfinite(scale)) return SGDN_EINVAL;
+  if (!isfinite(scale * 1.4426950408889634f)) return SGDN_EINVAL;
+  if (too_many_units(p)) return SGDN_EUNSUPPORTED;
   if (p->rows == 0) return SGDN_OK;
   if (!q || !k_cache || !v_cache || !table || !row_len || !o) return SGDN_EINVAL;
   if (row_req == nullptr && p->rows > p->batch) return SGDN_EINVAL;
@@ -177,8 +190,8 @@ int sgdn_paged_write(const sgdn_paged* p, const void* k, const void* v, int64_t 
 
 size_t sgdn_paged_workspace_bytes(const sgdn_paged* p, int32_t n_blocks, int32_t select) {
   if (check_read(p) != SGDN_OK || n_blocks < 0 || n_blocks > MAX_LIST) return 0;
-  if (select == 0) return attend_plan(p, n_blocks, true).total;   // without row_req no more
-  if (n_blocks < 1 || (longest(p) + p->page - 1) / p->page > MAX_NB) return 0;
+  if (select == 0) return too_many_units(p) ? 0 : attend_plan(p, n_blocks, true).total;   // without row_req no more
+  if (n_blocks < 1 || (longest(p) + p->page - 1) / p->page > MAX_NB || too_many_picks(p)) return 0;
   return select_bytes(p, n_blocks);
 }
 
@@ -212,7 +225,7 @@ int sgdn_paged_select(const sgdn_paged* p, const void* q, int64_t ldq, const int
   if (n_blocks > MAX_LIST) return SGDN_EUNSUPPORTED;
   if ((int64_t)n_sink + n_local > n_blocks) return SGDN_EINVAL;
   const int nb = (longest(p) + p->page - 1) / p->page;
-  if (nb > MAX_NB) return SGDN_EUNSUPPORTED;
+  if (nb > MAX_NB || too_many_picks(p)) return SGDN_EUNSUPPORTED;
   if (p->rows == 0) return SGDN_OK;
   if (!q || !codes || !scale || !table || !row_len || !blocks) return SGDN_EINVAL;
   if (row_req == nullptr && p->rows > p->batch) return SGDN_EINVAL;

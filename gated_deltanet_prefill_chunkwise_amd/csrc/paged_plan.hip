@@ -203,8 +203,7 @@ hipError_t launch_paged_release(const ReleaseArgs& a, hipStream_t s) {
 hipError_t launch_paged_plan(const PagePlanArgs& a, hipStream_t s) {
   const bool one = a.B <= 1024 && a.R <= 1024;
   if (one) {
-    const int n = a.B <= 256 && a.R <= 1024 ? 256 : 1024;
-    hipLaunchKernelGGL((plan_kernel<true>), dim3(1), dim3(n), 0, s, a);
+    hipLaunchKernelGGL((plan_kernel<true>), dim3(1), dim3(a.B <= 256 ? 256 : 1024), 0, s, a);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((plan_kernel<false>), dim3(1), dim3(a.B <= 256 ? 256 : 1024), 0, s, a);

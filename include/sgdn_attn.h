@@ -36,6 +36,7 @@
  * - Device data is never trusted with an address: a page outside
  *   [0, n_pages), a block outside the row's context and a slot outside the
  *   cache take no part (nothing is read or written for them).
+ * - Outputs overlap no inputs, except where said.
  * - Masked places are never read into a result: what unused slots and pages
  *   hold, NaN and infinities included, does not matter.
  * - Types: q, k, v and the caches share one of fp32, bf16, fp16; o is any of
@@ -59,8 +60,10 @@ extern "C" {
 #endif
 
 /* Shape of a call.  Supported: D in {64, 128, 256}, P in {16, 32, 64, 128},
- * Hq a multiple of Hkv, W P < 2^31, n_pages P < 2^31 (SGDN_EUNSUPPORTED
- * otherwise; non-positive values are SGDN_EINVAL, rows = 0 does nothing). */
+ * Hq a multiple of Hkv, W P < 2^31, n_pages P < 2^31, R Hq < 2^28, and
+ * R Hkv ceil(Hq / (16 Hkv)) < 2^24 - 8 for the attention, R Hkv < 2^22 - 8 for
+ * the choice of blocks (SGDN_EUNSUPPORTED otherwise; non-positive values are
+ * SGDN_EINVAL, rows = 0 does nothing). */
 typedef struct {
   int32_t rows;      /* R: rows of q (or k, v)                               */
   int32_t batch;     /* B: rows of the block table                           */
@@ -154,7 +157,7 @@ size_t sgdn_paged_workspace_bytes(const sgdn_paged* p, int32_t n_blocks, int32_t
  *   q            [R, Hq, D] with row stride ldq in elements
  *   table        [B, W]
  *   row_req      [R] or NULL (request r; R <= B);  row_len [R]
- *   scale        of the scores, finite
+ *   scale        of the scores, finite (also times log2(e))
  *   o            [R, Hq, D] o_dtype
  *   lse          [R, Hq] fp32 natural logarithm of the sum of exp(scale q.k),
  *                or NULL

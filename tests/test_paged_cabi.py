@@ -120,7 +120,7 @@ def test_attend_arguments(L):
             assert _attend(L, sparse=sparse, **{name: None}) == EINVAL, name
         for name in ("q", "kc", "vc", "o", "ws"):
             assert _attend(L, sparse=sparse, **{name: ODD}) == EINVAL, name
-        for scale in (float("nan"), float("inf")):
+        for scale in (float("nan"), float("inf"), 3e38):               # 3e38 log2(e) passes fp32
             assert _attend(L, sparse=sparse, scale=scale) == EINVAL
         for ldq in (8 * 128 - 8, 8 * 128 + 4, -1024):
             assert _attend(L, sparse=sparse, ldq=ldq) == EINVAL
@@ -133,6 +133,23 @@ def test_attend_arguments(L):
     assert _attend(L, sparse=True, blocks=None) == EINVAL
     assert L.sgdn_paged_attend(None, FAKE, 1024, FAKE, FAKE, FAKE, FAKE, FAKE, 1.0, FAKE, None,
                                FAKE, 1 << 40, None) == EINVAL
+
+
+def test_more_rows_than_a_launch_holds(L):
+    """A launch holds fewer than 2^32 threads."""
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    for kw in (dict(rows=(1 << 22) - 1, n_q=4, n_kv=4), dict(rows=1 << 21, n_q=80, n_kv=4)):   # 2^24 units of 256
+        s = _shape(batch=kw["rows"], **kw)
+        for sparse in (False, True):
+            assert _attend(L, s, sparse=sparse, ldq=kw["n_q"] * 128) == EUNSUPPORTED
+        assert ops.paged_workspace_bytes(s) == 0 and ops.paged_workspace_bytes(s, 4) == 0
+    s = _shape(rows=(1 << 22) - 3, batch=4, n_q=4, n_kv=4)
+    assert _attend(L, s, q=None, ldq=512) == EINVAL                     # enough room: the next check
+    for n, ok in ((1 << 20, False), ((1 << 20) - 4, True)):
+        s = _shape(rows=n, batch=4, n_q=4, n_kv=4)
+        assert _select(L, s, q=None, ldq=512) == (EINVAL if ok else EUNSUPPORTED)
+        assert (ops.paged_workspace_bytes(s, 4, True) > 0) == ok
+    assert _write(L, _shape(rows=1 << 28, n_q=1, n_kv=1)) == EUNSUPPORTED
 
 
 def test_attend_workspace(L):
