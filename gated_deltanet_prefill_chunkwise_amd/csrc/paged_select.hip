@@ -16,7 +16,7 @@
 // 64, 32/8 heads of 128: 18.3 us for 45 MB of codes and scales, 1/128 of the
 // keys and values, then 11.6 to pick 64); prompts by vector instructions, a
 // maximum over heads and a store for each score that the products make (6378
-// rows of 4 requests, up to 256 pages, 16/2 of 256: 48 us, and 14 to pick 16).
+// rows of 4 requests, up to 256 pages, 16/2 of 256: 31 us, and 14 to pick 16).
 #include <type_traits>
 
 #include "common.h"
@@ -142,8 +142,7 @@ template <typename E, int NS> __device__ __forceinline__ void products(const Que
   for (int j = 0; j < 4; ++j) v[j] = (float)acc[j] * q.sr[j];
 }
 __device__ __forceinline__ float scaled(float x, float sk) {
-  const float y = x * sk;
-  return y == y ? y : -INFINITY;
+  return fmaxf(x * sk, -INFINITY);                       // NaN: -infinity
 }
 
 // Rows of a request each (decode): the waves of a workgroup take HS heads,
@@ -216,17 +215,32 @@ __global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, in
 }
 
 // Many rows of a request (prompts), G <= 16: a tile holds 16 / GP tokens (GP: G
-// rounded up to a power of two), a wave QT tiles, which all use the pages that
-// it loads.  Tokens of different requests in a wave are taken request by
-// request.
-constexpr int tiles_of_wave(int gp) { return gp == 1 ? 2 : 4; }   // QT (a lane's addresses fill the registers at GP 1)
+// rounded up to a power of two), a wave QT tiles.  The workgroup takes pages in
+// stages of 32 through registers into two LDS buffers, the next on its way.
+// (Read by each wave from global memory, a page's 16 bytes for each lane are an
+// access of the L1 each: 45 million for 8192 rows and 1024 pages of two heads,
+// 73 us of 99; now 74 us, with vector instructions in front.  4 tiles a wave:
+// 117, though fewer workgroups read the codes; 64 pages a stage and 8 waves: 67
+// there and no change below 4000 rows.)  Tokens of different requests are taken request by request.
+constexpr int QT = 2;      // 16-row tiles of a wave
+constexpr int SP = 32;     // pages of a stage
+
+// Position of 16-byte unit c of page p's codes: an LDS access reads the pages
+// whose bit 2 is the same, and finds its units in different banks.
+template <int D> __device__ __forceinline__ int unit_at(int p, int c) {
+  return p * (D / 16) + (c ^ (D == 64 ? ((p >> 1) & 1) | ((p >> 2) & 2) : (p & 3) | ((p >> 1) & 4)));
+}
+
 template <typename E, int D, int GP>
-__global__ __launch_bounds__(64 * SW, D == 256 ? 2 : 3) void score_rows_kernel(PageSelectArgs a) {
-  constexpr int NS = D / 64, QT = tiles_of_wave(GP), TT = 16 / GP, TW = QT * TT;
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+__global__ __launch_bounds__(64 * SW, sizeof(E) == 4 ? 2 : 4) void score_rows_kernel(PageSelectArgs a) {
+  constexpr int NS = D / 64, TT = 16 / GP, TW = QT * TT;
+  constexpr int ROWS = SW * TW, RW = (ROWS + 63) / 64;   // of the workgroup; a lane's of them
+  constexpr int RU = D / 16, NU = (SP * RU + 255) / 256; // units of a page; a thread's of a stage
+  __shared__ V16 codes[2][SP * RU];
+  __shared__ float scales[2][SP];
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, g = lane >> 4;
-  const int row0 = (blockIdx.x * SW + wave) * TW, h = blockIdx.y;
-  if (row0 >= a.R) return;
+  const int wg0 = blockIdx.x * ROWS, row0 = wg0 + wave * TW, h = blockIdx.y;
   Query<E, NS> q[QT];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
@@ -234,25 +248,43 @@ __global__ __launch_bounds__(64 * SW, D == 256 ? 2 : 3) void score_rows_kernel(P
     RawQ<E, NS> raw;                                     // rows and heads beyond the last: the last again
     raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + hd) * D + 16 * g);
     quantise<E, NS>(raw, g, q[t]);
+    if (sizeof(E) == 4) asm volatile("" ::: "memory");   // not all tiles' raw elements at once
   }
-  // lane l: request and length of the wave's token l
-  int req = -1, len = 0;
-  if (lane < TW && row0 + lane < a.R) {
-    req = a.row_req[row0 + lane];
-    len = min(a.row_len[row0 + lane], a.max_len);
-    if (req < 0 || req >= a.B || len <= 0) req = -1;
+  // every wave goes through the rows of the workgroup; lane l: rows l and l + 64
+  int req[RW], len[RW];
+  uint64_t todo[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const int l = 64 * i + lane;
+    req[i] = -1;
+    len[i] = 0;
+    if (l < ROWS && wg0 + l < a.R) {
+      req[i] = a.row_req[wg0 + l];
+      len[i] = min(a.row_len[wg0 + l], a.max_len);
+      if (req[i] < 0 || req[i] >= a.B || len[i] <= 0) req[i] = -1;
+    }
+    todo[i] = __ballot(req[i] >= 0);
   }
-  uint64_t todo = __ballot(req >= 0);
-  while (todo != 0) {
-    const int now = __builtin_amdgcn_readlane(req, __builtin_ctzll(todo));
-    const uint64_t mine = __ballot(req == now) & todo;
-    todo &= ~mine;
-    int most = req == now ? len : 0;
+  while (true) {
+    int now = -1;
+#pragma unroll
+    for (int i = RW - 1; i >= 0; --i)
+      if (todo[i] != 0) now = __builtin_amdgcn_readlane(req[i], __builtin_ctzll(todo[i]));
+    if (now < 0) return;
+    int most = 0;
+    uint32_t mine = 0;                                   // by the wave's tokens
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const uint64_t of = __ballot(req[i] == now) & todo[i];
+      todo[i] &= ~of;
+      if ((wave * TW) >> 6 == i) mine = (uint32_t)(of >> ((wave * TW) & 63)) & (uint32_t)((1ull << TW) - 1);
+      if (req[i] == now) most = max(most, len[i]);
+    }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) most = max(most, __shfl_xor(most, o, 64));
     const int nb = __builtin_amdgcn_readfirstlane((most + (1 << a.lp) - 1) >> a.lp);
     const int32_t* table = a.table + (size_t)now * a.W;
-    const int step = 32 * gridDim.z, first = 32 * blockIdx.z;
+    const int step = SP * gridDim.z, first = SP * blockIdx.z;
     if (first >= nb) continue;
     // where this lane's scores go, by tile, and whether they are of this request
     constexpr int PER = GP >= 4 ? 1 : 4 / GP;            // tokens of a lane's four rows
@@ -266,45 +298,78 @@ __global__ __launch_bounds__(64 * SW, D == 256 ? 2 : 3) void score_rows_kernel(P
         ours[t][i] = (4 * g) % GP == 0 || GP < 4 ? ((mine >> tok) & 1) != 0 : false;
         to[t][i] = a.score + ((size_t)(row0 + tok) * a.Hkv + h) * a.NB + n;
       }
-    // two groups at a time; the next two, and the page numbers behind, on their way
-    Pages<NS> next[2];
-    int page[2];
+    // this thread's units tid, tid + 256 of a stage; wave 0 has the scales too
+    int page[NU], spage = 0, held = 0;
+    V16 unit[NU];
+    float scale = 0.f;
+    auto look_up = [&](int p0) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_pages<NS>(a, table[min(first + 16 * u + n, nb - 1)], h, g, next[u]);
+      for (int i = 0; i < NU; ++i) page[i] = table[min(p0 + ((tid + 256 * i) / RU) % SP, nb - 1)];
+      if (wave == 0) spage = table[min(p0 + tid % SP, nb - 1)];
+    };
+    auto fetch = [&]() {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) page[u] = table[min(first + step + 16 * u + n, nb - 1)];
-    for (int p0 = first; p0 < nb; p0 += step) {
-      const Pages<NS> pg[2] = {next[0], next[1]};
-      if (p0 + step < nb) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) load_pages<NS>(a, page[u], h, g, next[u]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) page[u] = table[min(p0 + 2 * step + 16 * u + n, nb - 1)];
+      for (int i = 0; i < NU; ++i) {
+        const size_t at = (size_t)(page[i] >= 0 && page[i] < a.n_pages ? page[i] : 0) * a.Hkv + h;
+        unit[i] = ldv(a.codes + at * D + 16 * ((tid + 256 * i) % RU));
       }
+      if (wave == 0) scale = a.scale[(size_t)(spage >= 0 && spage < a.n_pages ? spage : 0) * a.Hkv + h];
+      held = spage;
+    };
+    auto store = [&](int buf) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bool in = p0 + 16 * u + n < nb;
+      for (int i = 0; i < NU; ++i) {
+        const int u = tid + 256 * i;
+        if (u < SP * RU) codes[buf][unit_at<D>(u / RU, u % RU)] = unit[i];
+      }
+      if (tid < SP) scales[buf][tid] = held >= 0 && held < a.n_pages ? scale : __builtin_nanf("");   // which no maximum takes
+    };
+    look_up(first);
+    fetch();
+    look_up(first + step);
+    lds_barrier();                                       // the last request's stages have been read
+    store(0);
+    lds_barrier();
+    int buf = 0;
+    for (int p0 = first; p0 < nb; p0 += step) {
+      const bool more = p0 + step < nb;
+      if (more) {
+        fetch();
+        look_up(p0 + 2 * step);
+      }
+      if (mine != 0) {
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          float v[4];
-          products<E, NS>(q[t], pg[u], v);
-          float x[PER];
-          if constexpr (GP >= 4) {
-            x[0] = max2(max2(v[0], v[1]), max2(v[2], v[3]));
-            if (GP >= 8) x[0] = max_x16(x[0]);
-            if (GP == 16) x[0] = max_x32(x[0]);
-          } else if constexpr (GP == 2) {
-            x[0] = max2(v[0], v[1]);
-            x[1] = max2(v[2], v[3]);
-          } else {
+        for (int u = 0; u < 2; ++u) {
+          const bool in = p0 + 16 * u + n < nb;
+          Pages<NS> pg;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = v[i];
+          for (int s = 0; s < NS; ++s) pg.c[s] = __builtin_bit_cast(i32x4, codes[buf][unit_at<D>(16 * u + n, 4 * s + g)]);
+          pg.sk = scales[buf][16 * u + n];
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            float v[4];
+            products<E, NS>(q[t], pg, v);
+            float x[PER];
+            if constexpr (GP >= 4) {
+              x[0] = max2(max2(v[0], v[1]), max2(v[2], v[3]));
+              if (GP >= 8) x[0] = max_x16(x[0]);
+              if (GP == 16) x[0] = max_x32(x[0]);
+            } else if constexpr (GP == 2) {
+              x[0] = max2(v[0], v[1]);
+              x[1] = max2(v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = v[i];
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (in && ours[t][i]) to[t][i][p0 + 16 * u] = scaled(x[i], pg.sk);
           }
-#pragma unroll
-          for (int i = 0; i < PER; ++i)
-            if (in && ours[t][i]) to[t][i][p0 + 16 * u] = scaled(x[i], pg[u].sk);
         }
       }
+      if (more) store(buf ^ 1);
+      lds_barrier();
+      buf ^= 1;
     }
   }
 }
@@ -478,16 +543,17 @@ __global__ __launch_bounds__(NWV == 1 ? 256 : 64 * NWV) void pick_kernel(PageSel
 }
 
 template <typename E, int D> hipError_t launch_score_d(const PageSelectArgs& a, hipStream_t s) {
-  // Several rows of a request share its pages, if there are enough of them to
-  // fill the chip; otherwise (or with more heads than a tile) a row at a time.
-  // Shared and alone, 512 blocks, 32/8 heads of 128: 32 requests with 2, 4, 8
-  // and 32 rows each 41 and 19, 33 and 29, 29 and 39, 42 and 119 us; 256 with 4
-  // each 61 and 119; 1 request with 16, 64, 128 rows 16 and 12, 19 and 18, 21
-  // and 26; 16/2 heads of 256: 16 with 16 each (1000 blocks) 26 and 35.
-  if (a.R >= 4 * (int64_t)a.B && (int64_t)a.R * a.Hkv * D >= 1 << 17 && a.G <= 16) {
-    int gp = 1;
-    while (gp < a.G) gp <<= 1;
-    const unsigned per = tiles_of_wave(gp) * SW * (16 / gp), gx = (a.R + per - 1) / per;
+  // Rows of a request share its pages if they fill a quarter of a workgroup
+  // (which takes its requests one after the other) and all rows the chip;
+  // otherwise, or with more heads than a tile, a row at a time.  Shared and
+  // alone, 512 blocks, 32/8 heads of 128: 32 requests with 2, 4, 6, 8 and 32 rows
+  // each 55 and 19, 39 and 29, 37 and 36, 31 and 38, 39 and 104 us; 1 request
+  // with 16, 64, 128 rows 14 and 12, 16 and 19, 18 and 26; 16/2 heads of 256: 16
+  // with 16 each (1000 blocks) 20 and 35; 8/8 of 64: 64 with 8 each 87 and 46.
+  int gp = 1;
+  while (gp < a.G) gp <<= 1;
+  if ((int64_t)a.R * gp >= 32 * (int64_t)a.B && (int64_t)a.R * a.Hkv * D >= 1 << 16 && a.G <= 16) {
+    const unsigned per = QT * SW * (16 / gp), gx = (a.R + per - 1) / per;
     const unsigned want = (512 + gx * a.Hkv - 1) / (gx * a.Hkv), most = (a.NB + 127) / 128;
     const dim3 grid(gx, a.Hkv, want < most ? want : most);
     switch (gp) {
