@@ -145,30 +145,20 @@ __device__ __forceinline__ float scaled(float x, float sk) {
   return fmaxf(x * sk, -INFINITY);                       // NaN: -infinity
 }
 
-// Rows of a request each (decode): the waves of a workgroup take HS heads,
-// whose codes of a page are neighbours, and divide the row's pages by what is
-// left.  A workgroup takes one of Z shares of the pages; the shares of all
-// heads follow each other on one XCD (workgroup id mod 8), which then reads a
-// page's scales once.  A wave has a batch of four page groups on its way and
-// looks up the next, the first before it turns to its query, as nearly all of
-// its time is waiting.
-template <typename E, int D>
-__global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, int HS, int Z) {
-  constexpr int NS = D / 64, PG = 4;
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int n = lane & 15, g = lane >> 4;
-  const int HB = (a.Hkv + HS - 1) / HS, PS = SW / HS;
-  const int k = blockIdx.x >> 3, unit = (k / HB) * 8 + (blockIdx.x & 7);
-  const int r = unit / Z, share = unit - r * Z;
-  const int h = (k % HB) * HS + wave % HS;
-  if (r >= a.R || h >= a.Hkv) return;
+// One wave's share of the pages of row r and head h.  It has a batch of PG
+// page groups on its way and looks up the next, the first before it turns to
+// its query, as nearly all of its time is waiting.
+template <typename E, int D, int PG>
+__device__ __forceinline__ void score_row(const PageSelectArgs& a, int r, int h, int share, int shares) {
+  constexpr int NS = D / 64;
+  const int lane = lane_id(), n = lane & 15, g = lane >> 4;
   const int req = a.row_req == nullptr ? r : a.row_req[r];
   const int len = min(a.row_len[r], a.max_len);
   if (req < 0 || req >= a.B || len <= 0) return;
   const int nb = (len + (1 << a.lp) - 1) >> a.lp;
   const int32_t* table = a.table + (size_t)req * a.W;
   float* to = a.score + ((size_t)r * a.Hkv + h) * a.NB;
-  const int step = 16 * PG * PS * Z, first = 16 * PG * (share * PS + wave / HS);
+  const int step = 16 * PG * shares, first = 16 * PG * share;
   if (first >= nb) return;
   for (int h0 = 0; h0 < a.G; h0 += 16) {
     RawQ<E, NS> raw;                                     // heads beyond the group: the last one again
@@ -214,6 +204,21 @@ __global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, in
   }
 }
 
+// Rows of a request each (decode): the waves of a workgroup take HS heads,
+// whose codes of a page are neighbours, and divide the row's pages by what is
+// left.  A workgroup takes one of Z shares of the pages; the shares of all
+// heads follow each other on one XCD (workgroup id mod 8), which then reads a
+// page's scales once.
+template <typename E, int D>
+__global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, int HS, int Z) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int HB = (a.Hkv + HS - 1) / HS, PS = SW / HS;
+  const int k = blockIdx.x >> 3, unit = (k / HB) * 8 + (blockIdx.x & 7);
+  const int r = unit / Z, share = unit - r * Z;
+  const int h = (k % HB) * HS + wave % HS;
+  if (r < a.R && h < a.Hkv) score_row<E, D, 4>(a, r, h, share * PS + wave / HS, PS * Z);
+}
+
 // Many rows of a request (prompts), G <= 16: a tile holds 16 / GP tokens (GP: G
 // rounded up to a power of two), a wave QT tiles.  The workgroup takes pages in
 // stages of 32 through registers into two LDS buffers, the next on its way.
@@ -221,7 +226,9 @@ __global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, in
 // access of the L1 each: 45 million for 8192 rows and 1024 pages of two heads,
 // 73 us of 99; now 74 us, with vector instructions in front.  4 tiles a wave:
 // 117, though fewer workgroups read the codes; 64 pages a stage and 8 waves: 67
-// there and no change below 4000 rows.)  Tokens of different requests are taken request by request.
+// there and no change below 4000 rows.)  Tokens of different requests are taken request by request,
+// and where they are more than a few (new tokens of other requests behind a
+// prompt), row by row, each wave its own.
 constexpr int QT = 2;      // 16-row tiles of a wave
 constexpr int SP = 32;     // pages of a stage
 
@@ -241,15 +248,6 @@ __global__ __launch_bounds__(64 * SW, sizeof(E) == 4 ? 2 : 4) void score_rows_ke
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, g = lane >> 4;
   const int wg0 = blockIdx.x * ROWS, row0 = wg0 + wave * TW, h = blockIdx.y;
-  Query<E, NS> q[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int r = min(row0 + t * TT + n / GP, a.R - 1), hd = min(n % GP, a.G - 1);
-    RawQ<E, NS> raw;                                     // rows and heads beyond the last: the last again
-    raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + hd) * D + 16 * g);
-    quantise<E, NS>(raw, g, q[t]);
-    if (sizeof(E) == 4) asm volatile("" ::: "memory");   // not all tiles' raw elements at once
-  }
   // every wave goes through the rows of the workgroup; lane l: rows l and l + 64
   int req[RW], len[RW];
   uint64_t todo[RW];
@@ -264,6 +262,27 @@ __global__ __launch_bounds__(64 * SW, sizeof(E) == 4 ? 2 : 4) void score_rows_ke
       if (req[i] < 0 || req[i] >= a.B || len[i] <= 0) req[i] = -1;
     }
     todo[i] = __ballot(req[i] >= 0);
+  }
+  int runs = 0, last = -1;                               // runs of rows of one request
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    int before = __shfl_up(req[i], 1, 64);
+    if (lane == 0) before = last;
+    last = __builtin_amdgcn_readlane(req[i], 63);
+    runs += __builtin_popcountll(__ballot(req[i] >= 0 && req[i] != before));
+  }
+  if (runs > 4) {
+    for (int i = 0; i < TW && row0 + i < a.R; ++i) score_row<E, D, D == 256 ? 2 : 4>(a, row0 + i, h, blockIdx.z, gridDim.z);
+    return;
+  }
+  Query<E, NS> q[QT];
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    const int r = min(row0 + t * TT + n / GP, a.R - 1), hd = min(n % GP, a.G - 1);
+    RawQ<E, NS> raw;                                     // rows and heads beyond the last: the last again
+    raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + hd) * D + 16 * g);
+    quantise<E, NS>(raw, g, q[t]);
+    if (sizeof(E) == 4) asm volatile("" ::: "memory");   // not all tiles' raw elements at once
   }
   while (true) {
     int now = -1;

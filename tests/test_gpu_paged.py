@@ -420,6 +420,26 @@ def test_select_many_rows_of_requests(Hq, Hkv, D, dtype):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("Hq, Hkv, D", [(2, 2, 128), (8, 2, 64), (16, 2, 256), (16, 1, 128)])
+def test_select_prompt_and_single_rows(Hq, Hkv, D):
+    """A prompt between new tokens of other requests, more of them than a workgroup takes one by one."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    rng = np.random.default_rng(D)
+    P, W, B = 16, 37, 60
+    codes, scale, dc, ds = _summaries(rng, B * W, Hkv, D)
+    table = rng.permutation(B * W).reshape(B, W).astype(np.int32)
+    n = (1 << 17) // (Hkv * D) + 2 * B * B
+    req = np.r_[np.arange(1, 30), np.zeros(n), np.arange(30, B), -1].astype(np.int32)
+    length = rng.integers(1, W * P + 1, len(req)).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((len(req), Hq, D))).cuda().bfloat16()
+    got = ops.paged_select(q, dc, ds, _i32(table), _i32(length), P, 8, row_req=_i32(req))
+    torch.cuda.synchronize()
+    rows = np.r_[np.arange(0, 64), rng.integers(64, n, 200), np.arange(len(req) - 64, len(req))]
+    want = ref.select(_f64(q[rows]), codes, scale, table, length[rows], P, 8, req=req[rows])
+    assert np.array_equal(got.cpu().numpy()[rows], want)
+
+
 def test_select_values_that_are_not_finite():
     import torch
     from gated_deltanet_prefill_chunkwise_amd import ops
