@@ -37,6 +37,8 @@
 // tokens, 16/2 heads of 256, fp16: 88 us for 489 MB and 5 for the join; 32 rows
 // of 64 of up to 512 blocks of 64, 32/8 of 128: 96 us for 536 MB and 5.  One
 // row of 4096 tokens, 32/8 of 128: 7.2 and 3.9 us, latency.
+#include <type_traits>
+
 #include "common.h"
 #include "paged.h"
 
@@ -190,16 +192,20 @@ __device__ __forceinline__ void attend_unit(const PageAttendArgs& a, int unit, i
 
   int slot = 0;                       // lane of the current tile's look-up
   look_up(t0);
+  // The query, here: waited for inside the loop it would wait for what follows it too.
+  __builtin_amdgcn_s_waitcnt(0x0F70);                    // vmcnt(0)
   Half h0 = half(0), h1 = half(1);
   if (t0 < t1) { load_k(h0, h1); load_v(h0, h1); }
-  for (int t = t0; t < t1; t += NW) {
+  // A tile, and (MORE) the requests of the next one.  The last tile is a copy
+  // of its own: where a request may or may not follow another, a wait for the
+  // older one has to be a wait for both (32 rows of 64 listed blocks 95 us, so 91).
+  auto step = [&](int t, auto MORE) {
     f32x4 s0 = zero4(), s1 = zero4();
 #pragma unroll
     for (int s = 0; s < NS; ++s) { s0 = mma(kf[0][s], qf[s], s0); s1 = mma(kf[1][s], qf[s], s1); }
     const Half c0 = h0, c1 = h1;
     slot += 2;
-    const bool more = t + NW < t1;
-    if (more) {
+    if constexpr (MORE) {
       if (slot == 64) { look_up(t + NW); slot = 0; }
       h0 = half(slot);
       h1 = half(slot + 1);
@@ -252,8 +258,11 @@ __device__ __forceinline__ void attend_unit(const PageAttendArgs& a, int unit, i
         if (TWO) acc[i] = mma(vt, pl, acc[i]);
       }
     }
-    if (more) load_v(h0, h1);
-  }
+    if constexpr (MORE) load_v(h0, h1);
+  };
+  int t = t0;
+  for (; t + NW < t1; t += NW) step(t, std::true_type{});
+  if (t < t1) step(t, std::false_type{});
 
   // join the four waves
   l += __shfl_xor(l, 16, 64);
@@ -321,10 +330,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
 // workgroup for each row takes 28 us to find that out (8192 rows and heads);
 // so 2048 workgroups look 64 of their units up at a time.  Whole calls of 4096
 // rows of 16 of 256 blocks, a workgroup a row and so: 171 and 146 us (32/8 heads
-// of 128, nothing left), 160 and 155 (16/2 of 256); 1208 and 1275, 715 and 764
-// where every row is left, as the work is dealt out ahead.
+// of 128, nothing left), 160 and 155 (16/2 of 256); 1208 and 1247, 715 and 761
+// where every row is left, as the work is dealt out ahead.  (D = 256: one wave
+// a SIMD, as two leave too few registers for the loop.)
 template <typename E, typename O, int D>
-__global__ __launch_bounds__(64 * NW, 2) void left_kernel(PageAttendArgs a, int units) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void left_kernel(PageAttendArgs a, int units) {
   __shared__ Joined<D> lds;
   const int all = (units + 7) / 8 * 8;                   // a multiple of 8, like the grid
   for (int64_t first = blockIdx.x; first < all; first += 64 * (int64_t)gridDim.x) {
