@@ -356,10 +356,10 @@ __global__ __launch_bounds__(64 * SW, sizeof(E) == 4 ? 2 : 4) void score_rows_ke
         fetch();
         look_up(p0 + 2 * step);
       }
+      float x[2][QT][PER];
       if (mine != 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const bool in = p0 + 16 * u + n < nb;
           Pages<NS> pg;
 #pragma unroll
           for (int s = 0; s < NS; ++s) pg.c[s] = __builtin_bit_cast(i32x4, codes[buf][unit_at<D>(16 * u + n, 4 * s + g)]);
@@ -368,25 +368,35 @@ __global__ __launch_bounds__(64 * SW, sizeof(E) == 4 ? 2 : 4) void score_rows_ke
           for (int t = 0; t < QT; ++t) {
             float v[4];
             products<E, NS>(q[t], pg, v);
-            float x[PER];
+            float (&y)[PER] = x[u][t];
             if constexpr (GP >= 4) {
-              x[0] = max2(max2(v[0], v[1]), max2(v[2], v[3]));
-              if (GP >= 8) x[0] = max_x16(x[0]);
-              if (GP == 16) x[0] = max_x32(x[0]);
+              y[0] = max2(max2(v[0], v[1]), max2(v[2], v[3]));
+              if (GP >= 8) y[0] = max_x16(y[0]);
+              if (GP == 16) y[0] = max_x32(y[0]);
             } else if constexpr (GP == 2) {
-              x[0] = max2(v[0], v[1]);
-              x[1] = max2(v[2], v[3]);
+              y[0] = max2(v[0], v[1]);
+              y[1] = max2(v[2], v[3]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] = v[i];
+              for (int i = 0; i < 4; ++i) y[i] = v[i];
             }
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-              if (in && ours[t][i]) to[t][i][p0 + 16 * u] = scaled(x[i], pg.sk);
+            for (int i = 0; i < PER; ++i) y[i] = scaled(y[i], pg.sk);
           }
         }
       }
+      // The next stage before the scores go out: a wait for what was fetched
+      // would wait for them as well.
       if (more) store(buf ^ 1);
+      if (mine != 0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int t = 0; t < QT; ++t)
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (p0 + 16 * u + n < nb && ours[t][i]) to[t][i][p0 + 16 * u] = x[u][t][i];
+      }
       lds_barrier();
       buf ^= 1;
     }
