@@ -21,14 +21,14 @@
 // different requests, is left (done = 0) as well: that kernel runs behind and
 // reads for each row its own blocks only.
 //
-// Bound: the steps of a stage, which follow each other: 272 us for 4096 rows
-// of 16 of 256 blocks of 64 keys in four requests (16/2 heads of 256, bf16);
-// without the products or the exponentials 261, without the copies 215, without
-// the copies and the LDS reads 173.  (Their least is 41 us of products if each
-// row had only its own.)  Tried at those sizes and slower: 32 x 32 x 16
-// instructions (300), 64 columns a workgroup (285), all of K's LDS reads at once
-// (292), copies straight to LDS (395); 64-key stages of wave pairs that share
-// weights: 243, but 147 and not 118 at D = 128.
+// Bound: the steps of a stage, which follow each other, and LDS, which a wave
+// reads whole for its 16 or 32 columns.  3189 rows of 16 of up to 256 blocks of
+// 64 keys in four requests (16/2 heads of 256, bf16): 253 us, of which 114 are
+// the products at the unions' size (32 blocks in the mean, 55 at most) and 41
+// would be with each row's own blocks alone.  Tried and slower at D = 256, when
+// it took 272: 32 x 32 x 16 instructions (300), 64 columns a workgroup (285),
+// copies straight to LDS (395); 64-key stages of wave pairs that share weights:
+// 243, but 147 and not 118 at D = 128.
 #include "common.h"
 #include "paged.h"
 
@@ -332,15 +332,15 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
             const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
             return __builtin_bit_cast(frag_t<E>, v);
           };
-          // The values' reads before the weights are formed, where the registers
-          // hold them that long (D = 128: 126 -> 118 us; D = 256 spills).
-          constexpr bool EARLY = D < 256;
-          frag_t<E> vf[DT];
-          if (EARLY) {
+          // The values' reads: all before the weights are formed where the
+          // registers hold them that long (D = 128: 126 -> 118 us), else two, and
+          // the next two in front of the products of these (307 -> 276 us for the
+          // whole call below; four: 279, eight: 290).
+          constexpr int VB = D < 256 ? DT : 2;
+          frag_t<E> vf[2][VB];
 #pragma unroll
-            for (int d = 0; d < DT; ++d) vf[d] = value(d);
-            __builtin_amdgcn_sched_barrier(0);
-          }
+          for (int d = 0; d < VB; ++d) vf[0][d] = value(d);
+          __builtin_amdgcn_sched_barrier(0);
           frag_t<E> ph[CT], pl[CT];
 #pragma unroll
           for (int t = 0; t < CT; ++t) {
@@ -377,13 +377,19 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
             }
           }
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const frag_t<E> vt = EARLY ? vf[d] : value(d);
+          for (int d0 = 0; d0 < DT; d0 += VB) {
+            if (d0 + VB < DT) {
 #pragma unroll
-            for (int t = 0; t < CT; ++t) {
-              acc[t][d] = mma(vt, ph[t], acc[t][d]);
-              if (TWO) acc[t][d] = mma(vt, pl[t], acc[t][d]);
+              for (int d = 0; d < VB; ++d) vf[(d0 / VB + 1) & 1][d] = value(d0 + VB + d);
+              __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int d = 0; d < VB; ++d)
+#pragma unroll
+              for (int t = 0; t < CT; ++t) {
+                acc[t][d0 + d] = mma(vf[(d0 / VB) & 1][d], ph[t], acc[t][d0 + d]);
+                if (TWO) acc[t][d0 + d] = mma(vf[(d0 / VB) & 1][d], pl[t], acc[t][d0 + d]);
+              }
           }
         }
         if (more_stages) put(i + 1, a0, a1, buf ^ 1);
