@@ -27,16 +27,16 @@
 // largest weight.
 //
 // 16-bit weights enter the second product in two parts, the number rounded to
-// the type and what that left: the time stays (517, 93 and 97 us below), and o
+// the type and what that left: the time of the first three calls below stays, and o
 // errs by its own rounding only.
 //
 // Bound: HBM, each key and value once per row.  (At most 16 of 16 columns of
 // the products are used; at 16 heads a group that is 4 flops a byte.)
-// Measured: 128 rows of 2071 to 8192 tokens, 32/8 heads of 128, bf16: 518 us for
+// Measured: 128 rows of 2071 to 8192 tokens, 32/8 heads of 128, bf16: 516 us for
 // 2.67 GB (5.2 TB/s, what a copy of 1 GiB reaches); 2 rows of 106635 and 131072
-// tokens, 16/2 heads of 256, fp16: 88 us for 489 MB and 5 for the join; 32 rows
-// of 64 of up to 512 blocks of 64, 32/8 of 128: 96 us for 536 MB and 5.  One
-// row of 4096 tokens, 32/8 of 128: 7.2 and 3.9 us, latency.
+// tokens, 16/2 heads of 256, fp16: 87 us for 489 MB and 5 for the join; 32 rows
+// of 64 of up to 512 blocks of 64, 32/8 of 128: 95 us for 536 MB and 5.  One
+// row of 4096 tokens, 32/8 of 128: 6.9 and 3.8 us, latency.
 #include <type_traits>
 
 #include "common.h"
@@ -198,7 +198,7 @@ __device__ __forceinline__ void attend_unit(const PageAttendArgs& a, int unit, i
   if (t0 < t1) { load_k(h0, h1); load_v(h0, h1); }
   // A tile, and (MORE) the requests of the next one.  The last tile is a copy
   // of its own: where a request may or may not follow another, a wait for the
-  // older one has to be a wait for both (32 rows of 64 listed blocks 95 us, so 91).
+  // older one has to be a wait for both (1 to 2% of a call).
   auto step = [&](int t, auto MORE) {
     f32x4 s0 = zero4(), s1 = zero4();
 #pragma unroll

@@ -23,7 +23,7 @@
 //
 // Bound: the steps of a stage, which follow each other, and LDS, which a wave
 // reads whole for its 16 or 32 columns.  3189 rows of 16 of up to 256 blocks of
-// 64 keys in four requests (16/2 heads of 256, bf16): 253 us, of which 114 are
+// 64 keys in four requests (16/2 heads of 256, bf16): 241 us, of which 114 are
 // the products at the unions' size (32 blocks in the mean, 55 at most) and 41
 // would be with each row's own blocks alone.  Tried and slower at D = 256, when
 // it took 272: 32 x 32 x 16 instructions (300), 64 columns a workgroup (285),
@@ -42,17 +42,17 @@ constexpr int SK = 32;                 // keys of a stage
 // 256 elements their accumulators do not fit the registers.
 constexpr int tiles_of_wave(int d) { return d == 256 ? 1 : 2; }
 
-// What is left alone.  A block of the union costs a tile as much as GAIN
+// What is left alone.  A block of the union costs a tile as much as gain / 4
 // blocks of single rows' lists cost the kernel for these while the chip is
 // full; with fewer than `full` tiles the tiles still take as long as `full`
 // would, as a tile walks its union alone.  Tiles and single rows, 4096 rows of
 // 16 of 256 blocks of 64 keys, where 32, 4, 2 or 1 neighbouring rows have one
-// list: 32/8 heads of 128 172, 720, 1123, 1506 and 1148 to 1184 us; 16/2 of 256
-// (1024 rows: 76 and 158) 391, 653, 1075 for 4, 2, 1 and 595 to 695; 16/1 of 128
-// 77, 122, 192, 358 and 158 to 164; 8/8 of 64 163, 428 (8 alike), 612 (1) and 683.  256
-// rows that are all alike: 58 and 78 (32/8 of 128), 69 and 46 (16/2 of 256).
-constexpr int GAIN = 3;
-constexpr int full_of(int d) { return d == 256 ? 256 : 512; }
+// list: 32/8 heads of 128 149, 700, 1085, 1468 and 1139 to 1166 us; 16/2 of 256
+// (1024 rows: 72 and 159) 327, 538, 887 for 4, 2, 1 and 612 to 644; 16/1 of 128
+// 115 and 186 for 4 and 2 and 160; 8/8 of 64 138 and 591 (1) and 680.  256 rows
+// that are all alike: 58 and 79 (32/8 of 128), 65 and 45 (16/2 of 256).
+constexpr int gain_of(int d) { return d == 256 ? 9 : 12; }
+constexpr int full_of(int d) { return d == 256 ? 384 : 512; }
 constexpr int LIST = 256;              // blocks of the union that are listed at a time (8 words of bits)
 
 // Position of 16-byte unit c of row `key`.  An access reads the keys whose bit 2
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
       for (int i = lane; i < nw; i += 64) blocks += __builtin_popcount(uni[i]);
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) blocks += __shfl_xor(blocks, o, 64);
-      if (GAIN * (int64_t)__builtin_amdgcn_readfirstlane(blocks) * max(units, full_of(D)) > (int64_t)units * n_entries) {
+      if (gain_of(D) * (int64_t)__builtin_amdgcn_readfirstlane(blocks) * max(units, full_of(D)) > 4 * (int64_t)units * n_entries) {
         if (tid == 0) *done = 0;
         return;
       }
@@ -461,7 +461,7 @@ int paged_tile_rows(int R, int B, int G, int Hkv, int d, bool has_req, int dtype
   while (gp < G) gp <<= 1;
   const int tq = COLS / gp;
   const long long words = ((((long long)max_len - 1) >> lp) >> 5) + 1;
-  if ((long long)R * Hkv < GAIN * full_of(d) || (long long)tq * n_blocks > 32 * 256 || (tq + 1) * words * 4 > 15 * 1024) return 0;
+  if (4 * (long long)R * Hkv < gain_of(d) * full_of(d) || (long long)tq * n_blocks > 32 * 256 || (tq + 1) * words * 4 > 15 * 1024) return 0;
   return tq;
 }
 
