@@ -706,6 +706,46 @@ def test_attend_sparse_prompts(Hq, Hkv, D, P, K, dtype, out):
     check(o[i], lse[i], want, out, dtype, D)
 
 
+def test_far_pages_of_prompts():
+    """Tiles and the choice of blocks where offsets into the cache and the summaries pass 32 bits."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    P, Hkv, D, R = 64, 4, 128, 900
+    n_pages = (2 ** 31 + 2 ** 26) // (P * Hkv * D)
+    k = torch.empty((n_pages, Hkv, P, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    table = np.array([[n_pages - 1, 0, n_pages - 3, 2, n_pages - 2, 1] + list(range(n_pages - 20, n_pages - 8))], np.int32)
+    for p in table[0]:
+        k[int(p)], v[int(p)] = torch.randn((2, Hkv, P, D), generator=g, device="cuda").bfloat16()
+    q = torch.randn((R, 8, D), generator=g, device="cuda").bfloat16()
+    length = 200 + np.arange(R, dtype=np.int32)
+    lists = np.broadcast_to(np.array([0, 2, 3], np.int32), (R, Hkv, 3)).copy()
+    ws = torch.zeros(1 << 12, dtype=torch.uint8, device="cuda")
+    o, lse = ops.paged_attend_sparse(q, k, v, _i32(table), _i32(length), _i32(lists), row_req=_i32(np.zeros(R)), want_lse=True, workspace=ws)
+    torch.cuda.synchronize()
+    assert (ws.view(torch.int32) == 1).sum() >= 40
+    rows = np.r_[np.arange(0, R, 37), R - 1]
+    i = torch.from_numpy(rows).cuda()
+    at = torch.from_numpy(table[0]).long().cuda()
+    near = np.arange(table.shape[1], dtype=np.int32)[None]
+    want = ref.attend(_f64(q[i]), _f64(k[at]), _f64(v[at]), near, length[rows], np.zeros(len(rows), int), blocks=lists[rows])
+    check(o[i], lse[i], want, "f32", "bf16", D)
+    del k, v
+    n_pages = (2 ** 31 + 2 ** 27) // (Hkv * D)             # summaries are a P-th of the keys
+    codes = torch.zeros((n_pages, Hkv, D), dtype=torch.int8, device="cuda")
+    scale = torch.ones((n_pages, Hkv), device="cuda")
+    table = np.array([[n_pages - 1, 0, n_pages - 3, 2, n_pages - 2, 1] + list(range(n_pages - 20, n_pages - 8))], np.int32)
+    at = torch.from_numpy(table[0]).long().cuda()
+    codes[at] = torch.randint(-127, 128, (table.shape[1], Hkv, D), generator=g, device="cuda").to(torch.int8)
+    for n in (R, 3):                                       # rows that share pages, single rows
+        got = ops.paged_select(q[:n], codes, scale, _i32(table), _i32(length[:n]), P, 4, row_req=_i32(np.zeros(n)))
+        torch.cuda.synchronize()
+        pick = rows[rows < n]
+        want = ref.select(_f64(q)[pick], codes[at].cpu().numpy(), scale[at].cpu().numpy(), near, length[pick], P, 4, req=np.zeros(len(pick), int))
+        assert np.array_equal(got.cpu().numpy()[pick], want)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1e-3, 3.0])
 def test_attend_scale(scale):
     """Scales of either sign and 0, for single rows and for tiles of rows."""
