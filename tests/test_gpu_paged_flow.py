@@ -164,6 +164,50 @@ def _prompt_call(seed, rows=4200):
     return dict(q=q, k_cache=k, v_cache=v, table=_i32(table), row_len=_i32(length), blocks=_i32(lists), row_req=_i32(np.zeros(rows)))
 
 
+def test_captured_turnover():
+    """Release and a plan of more rows than one launch takes, in place, replayed on other states."""
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    n, w, page, rows, pages = 50, 12, 32, 3000, 700
+    rng = np.random.default_rng(31)
+
+    def state():
+        lens = rng.integers(0, 300, n).astype(np.int32)
+        table, ring, ids = np.full((n, w), -1, np.int32), np.zeros(pages, np.int32), rng.permutation(pages)
+        held = -(-lens // page)
+        for b in range(n):
+            table[b, :held[b]], ids = ids[:held[b]], ids[held[b]:]
+        taken = int(rng.integers(0, 10 * pages))
+        ring[(taken + np.arange(len(ids))) % pages] = ids
+        done = (rng.random(n) < 0.3).astype(np.uint8)
+        add = np.where(done, 0, rng.integers(0, 90, n)).astype(np.int32)
+        return dict(lens=lens, done=done, add=add, table=table, ring=ring, pos=np.array([taken, taken + len(ids)], np.int64))
+
+    d = {k: torch.from_numpy(x).cuda() for k, x in state().items()}
+
+    def call():
+        ops.paged_release(d["lens"], d["done"], d["table"], d["ring"], d["pos"], page, lens_out=d["lens"], free_pos_out=d["pos"])
+        return ops.paged_plan(d["lens"], d["add"], d["table"], d["ring"], d["pos"], page, rows, lens_out=d["lens"], free_pos_out=d["pos"])
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for _ in range(5):
+        s = state()
+        for k, x in s.items():
+            d[k].copy_(torch.from_numpy(x))
+        graph.replay()
+        torch.cuda.synchronize()
+        lens, ring, pos = ref.release(s["lens"], s["done"], s["table"], s["ring"], s["pos"], page)
+        want = ref.plan(lens, s["add"], s["table"], ring, pos, page, rows)
+        for k in ("lens", "cu", "page_cu", "slot", "row_req", "row_len", "status", "free_pos"):
+            assert np.array_equal(got[k].cpu().numpy(), want[k]), k
+        assert np.array_equal(d["table"].cpu().numpy(), want["table"]) and np.array_equal(d["ring"].cpu().numpy(), ring)
+        torch.ones(1 << 20, device="cuda").sum().item()
+
+
 def test_captured_prompts_and_shared_workspace():
     """Tiles, single rows and splits in two graphs that use one workspace in turn."""
     import torch
