@@ -329,9 +329,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
 // The rows that the tiles left, S = MT = 1.  Most often there are none, and a
 // workgroup for each row takes 28 us to find that out (8192 rows and heads);
 // so 2048 workgroups look 64 of their units up at a time.  Whole calls of 4096
-// rows of 16 of 256 blocks, a workgroup a row and so: 171 and 146 us (32/8 heads
-// of 128, nothing left), 160 and 155 (16/2 of 256); 1208 and 1247, 715 and 761
-// where every row is left, as the work is dealt out ahead.  (D = 256: one wave
+// rows of 16 of 256 blocks, a workgroup a row and so (tiles with weights in one
+// part): 171 and 146 us (32/8 heads of 128, nothing left), 160 and 155 (16/2 of
+// 256); 1208 and 1247, 715 and 761 where every row is left, as the work is dealt
+// out ahead.  (D = 256: one wave
 // a SIMD, as two leave too few registers for the loop.)
 template <typename E, typename O, int D>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void left_kernel(PageAttendArgs a, int units) {

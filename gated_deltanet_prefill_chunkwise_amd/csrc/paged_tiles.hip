@@ -21,14 +21,18 @@
 // different requests, is left (done = 0) as well: that kernel runs behind and
 // reads for each row its own blocks only.
 //
+// The softmax weights enter in two parts, as in paged_attend.hip, so that a
+// row errs alike whichever kernel takes it.  (One part is 241 us in the call
+// below, but rounds every weight to 16 bits: 1.4 times the error of a 16-bit o.)
+//
 // Bound: the steps of a stage, which follow each other, and LDS, which a wave
 // reads whole for its 16 or 32 columns.  3189 rows of 16 of up to 256 blocks of
-// 64 keys in four requests (16/2 heads of 256, bf16): 241 us, of which 114 are
+// 64 keys in four requests (16/2 heads of 256, bf16): 281 us, of which 171 are
 // the products at the unions' size (32 blocks in the mean, 55 at most) and 41
-// would be with each row's own blocks alone.  Tried and slower at D = 256, when
-// it took 272: 32 x 32 x 16 instructions (300), 64 columns a workgroup (285),
-// copies straight to LDS (395); 64-key stages of wave pairs that share weights:
-// 243, but 147 and not 118 at D = 128.
+// would be with each row's own blocks alone and each product once.  Tried and
+// slower at D = 256, when it took 272 with one part: 32 x 32 x 16 instructions
+// (300), 64 columns a workgroup (285), copies straight to LDS (395); 64-key stages
+// of wave pairs that share weights: 243, but 147 and not 118 at D = 128.
 #include "common.h"
 #include "paged.h"
 
@@ -45,13 +49,16 @@ constexpr int tiles_of_wave(int d) { return d == 256 ? 1 : 2; }
 // What is left alone.  A block of the union costs a tile as much as gain / 4
 // blocks of single rows' lists cost the kernel for these while the chip is
 // full; with fewer than `full` tiles the tiles still take as long as `full`
-// would, as a tile walks its union alone.  Tiles and single rows, 4096 rows of
-// 16 of 256 blocks of 64 keys, where 32, 4, 2 or 1 neighbouring rows have one
-// list: 32/8 heads of 128 149, 700, 1085, 1468 and 1139 to 1166 us; 16/2 of 256
-// (1024 rows: 72 and 159) 327, 538, 887 for 4, 2, 1 and 612 to 644; 16/1 of 128
-// 115 and 186 for 4 and 2 and 160; 8/8 of 64 138 and 591 (1) and 680.  256 rows
-// that are all alike: 58 and 79 (32/8 of 128), 65 and 45 (16/2 of 256).
-constexpr int gain_of(int d) { return d == 256 ? 9 : 12; }
+// would, as a tile walks its union alone.  All tiles and all single rows, 4096
+// rows of 16 of 256 blocks of 64 keys, where 32, 4, 3, 2 or 1 neighbouring rows
+// have one list: 32/8 heads of 128 173, 791, 1053, 1253, 1709 and 1137 to 1164
+// us; 16/2 of 256 154, 353, 517, 606, 990 and 599 to 639; 32/8 of 64 619, 920,
+// 1259 (4, 2, 1) and 684 to 694; 8/8 of 64 682 (1) and 679, with 16384 rows 1486
+// and 2697.  256 rows where 32 have one list: 66 and 77 (32/8 of 128), 52 and 48
+// (of 64), 70 and 45 (16/2 of 256; 512 rows 73 and 84).  Near the border a call of
+// which some tiles are left and some are not pays for both (16/2 of 256, 2 rows
+// alike, with gain 10: 1035), so 256 keeps 9, where these are all taken.
+constexpr int gain_of(int d) { return d == 256 ? 9 : d == 128 ? 14 : 16; }
 constexpr int full_of(int d) { return d == 256 ? 384 : 512; }
 constexpr int LIST = 256;              // blocks of the union that are listed at a time (8 words of bits)
 
@@ -74,10 +81,6 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
   constexpr int BUF = 2 * SK * D;      // elements of a stage: K, then V
   constexpr int RU = D / 8;            // 16-byte units of a row
   constexpr int NU = SK * 2 * RU / NT; // of a stage, for a thread
-  // Weights in two parts, as in paged_attend.hip, cost the matrix cores half as
-  // much again.  A 16-bit o errs by half a step of its type in any case, and
-  // weights rounded once add no more than that of the weighted mean of |v|.
-  constexpr bool TWO = sizeof(O) == 4;
   constexpr float BIAS = sizeof(E) == 2 && __is_same(E, fp16) ? 10.f : 0.f;   // see paged_attend.hip
   extern __shared__ __attribute__((aligned(16))) char lds[];
   E* stage = reinterpret_cast<E*>(lds);
@@ -333,9 +336,9 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
             return __builtin_bit_cast(frag_t<E>, v);
           };
           // The values' reads: all before the weights are formed where the
-          // registers hold them that long (D = 128: 126 -> 118 us), else two, and
+          // registers hold them that long (D = 128, one part: 126 -> 118 us), else two, and
           // the next two in front of the products of these (307 -> 276 us for the
-          // whole call below; four: 279, eight: 290).
+          // whole call above, with weights in one part; four: 279, eight: 290).
           constexpr int VB = D < 256 ? DT : 2;
           frag_t<E> vf[2][VB];
 #pragma unroll
@@ -373,7 +376,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
               const float p = __builtin_amdgcn_exp2f(fmaf(x[r], scale, -cs));
               l[t] += p;
               ph[t][r] = from_f<E>(p);
-              if (TWO) pl[t][r] = from_f<E>(p - to_f(ph[t][r]));
+              pl[t][r] = from_f<E>(p - to_f(ph[t][r]));
             }
           }
 #pragma unroll
@@ -388,7 +391,7 @@ __global__ __launch_bounds__(64 * (8 / tiles_of_wave(D)), 2) void tile_kernel(Pa
 #pragma unroll
               for (int t = 0; t < CT; ++t) {
                 acc[t][d0 + d] = mma(vf[(d0 / VB) & 1][d], ph[t], acc[t][d0 + d]);
-                if (TWO) acc[t][d0 + d] = mma(vf[(d0 / VB) & 1][d], pl[t], acc[t][d0 + d]);
+                acc[t][d0 + d] = mma(vf[(d0 / VB) & 1][d], pl[t], acc[t][d0 + d]);
               }
           }
         }

@@ -43,10 +43,10 @@
  *   them.  Products run on the matrix cores with fp32 accumulation; the
  *   softmax maximum, sum and the output accumulate in fp32.  With 16-bit
  *   inputs the softmax weights enter their product as two numbers of that type
- *   (weight and remainder), so that o errs by fp32's rounding and its own; only
- *   rows that share their lists (sgdn_paged_attend_sparse of many rows, 16-bit
- *   o) take weights rounded once to the type, half the products.  With fp32
- *   inputs nothing is rounded below fp32.
+ *   (weight and remainder), whichever kernel takes a row.  With fp32 inputs
+ *   nothing is rounded below fp32.  A row's bits may depend on the lists of its
+ *   neighbours (sgdn_paged_attend_sparse of many rows: rows that share their
+ *   lists are taken together, and sum in another order), its error bound not.
  * - Alignment: q, k, v, the caches, codes and o start at 16 bytes; row
  *   strides are multiples of 16 bytes.  Otherwise SGDN_EINVAL.
  */
