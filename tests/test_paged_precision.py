@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 
 from oracle import paged as ref
-from test_gpu_paged import U, _f64, _i32, _prompt, _t
+from test_gpu_paged import LENS, U, Case, _f64, _i32, _lists, _prompt, _t
 
 TWO_PARTS = {"bf16": (2.0 ** -17, 0.0), "f16": (2.0 ** -23, 2.0 ** -35)}
 
@@ -62,5 +62,25 @@ def test_rows_that_share_lists(Hq, Hkv, D, P, K, dtype, out):
     want = ref.attend(_f64(q[rows]), _f64(c.k), _f64(c.v), c.table, length[rows], req[rows], blocks=lists[rows])
     v = _f64(c.v)
     err = worst(_f64(o[torch.from_numpy(rows).cuda()]), want, out, dtype, D, np.abs(v[np.isfinite(v)]).max())
+    print(f"err / bound {err:.3f}")
+    assert err <= 1.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype, out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("Hq, Hkv, D, P", [(4, 1, 64, 16), (8, 2, 128, 64), (16, 1, 256, 64), (20, 1, 64, 32)])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_single_rows(Hq, Hkv, D, P, dtype, out, sparse):
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    c = Case(Hq + D + P + 2, LENS, Hq, Hkv, D, P, dtype)
+    q = c.q(len(LENS))
+    lists = _lists(c.rng, len(LENS), Hkv, 3, -(-c.lens // P)) if sparse else None
+    args = (q, c.k, c.v, _i32(c.table), _i32(c.lens))
+    o, _ = ops.paged_attend_sparse(*args, _i32(lists), out_dtype=_t(out)) if sparse else ops.paged_attend(*args, out_dtype=_t(out))
+    torch.cuda.synchronize()
+    want = ref.attend(_f64(q), _f64(c.k), _f64(c.v), c.table, c.lens, blocks=lists)
+    v = _f64(c.v)
+    err = worst(_f64(o), want, out, dtype, D, np.abs(v[np.isfinite(v)]).max())
     print(f"err / bound {err:.3f}")
     assert err <= 1.0
