@@ -4,9 +4,13 @@
 //   score(r, h, j) = max over the group's heads of (q8 . codes_j) sq scale_j
 // q8 and sq: the query's elements as 8-bit codes with a power of two, formed
 // as a page's summary is.  The products run on the 8-bit matrix cores with
-// 32-bit sums: |q8 . codes| <= 127^2 256 < 2^24, so the sum is exact, stays
-// exact as fp32 and under both powers of two; hence every evaluation order
-// gives the same score and the choice has no border cases.
+// 32-bit sums: |q8 . codes| <= 127^2 256 < 2^22, so the sum is exact, also as
+// fp32.  Only the order of a row's scores matters, so sq is taken over 2^16
+// times the group's largest: whatever the queries' size, no score passes fp32
+// (2^22 2^-16 2^121, the largest scale that a page has), and it is exact, all
+// multiples of 2^-149 being fp32 numbers, as long as sq / (largest sq) and that
+// times scale_j are >= 2^-133.  Hence every evaluation order gives the same
+// score and the choice has no border cases.
 //
 // score_*_kernel: 16 rows of A are (token, head) pairs, 16 columns of B pages.
 // pick_kernel: the K largest of a row by halving the range of
@@ -50,7 +54,8 @@ __device__ __forceinline__ float max_x32(float x) {
 }
 
 // A query tile as the A operand: lane (n, g) elements 64 s + 16 g .. + 15 of
-// row n, as codes; sr: the powers of two of D's rows 4g + j.
+// row n, as codes; sr: the powers of two of D's rows 4g + j, over 2^16 times
+// their group's largest.
 template <typename E, int NS> struct Query {
   i32x4 c[NS];
   float sr[4];
@@ -76,15 +81,15 @@ template <typename E, int NS> struct RawQ {
     }
   }
 };
-// Codes as the low byte of x 2^-e + 1.5 2^23, whose last place is 1: the sum
-// rounds to the nearest whole number, ties to even, in two's complement.
-template <typename E, int NS> __device__ __forceinline__ void quantise(const RawQ<E, NS>& raw, int g, Query<E, NS>& q) {
+// Largest |x| of row n; elements that are not finite count as 0.  `odd` (uniform):
+// there are some.
+template <typename E, int NS> __device__ __forceinline__ float peak(const RawQ<E, NS>& raw, bool& odd) {
   uint32_t top = 0u;                                    // |x| by its bits: NaN over infinity over numbers
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, __builtin_bit_cast(uint32_t, raw.at(s, i)) & 0x7fffffffu);
-  const bool odd = __ballot(top >= 0x7f800000u) != 0ull;   // uniform: some element counts as 0
+  odd = __ballot(top >= 0x7f800000u) != 0ull;
   if (odd) {
     top = 0u;
 #pragma unroll
@@ -95,9 +100,25 @@ template <typename E, int NS> __device__ __forceinline__ void quantise(const Raw
         if (u < 0x7f800000u) top = max(top, u);
       }
   }
-  const float t = max_x32(max_x16(__builtin_bit_cast(float, top)));
-  const int e = t == 0.f ? 0 : max(ilogbf(t) - 6, -126);
-  const float inv = ldexpf(1.f, -e), sq = ldexpf(1.f, e);   // normal numbers: -126 <= e <= 121
+  return max_x32(max_x16(__builtin_bit_cast(float, top)));
+}
+// Power of two of a row's codes by its peak.  (The codes of a row of zeros have
+// any; the least, as it takes part in its group's largest.)
+__device__ __forceinline__ int power_of(float t) { return t == 0.f ? -126 : max(ilogbf(t) - 6, -126); }
+// Largest of the rows n of a group, GP (a power of two) next to each other.
+template <int GP> __device__ __forceinline__ int group_max(int e) {
+#pragma unroll
+  for (int o = 1; o < GP; o <<= 1) e = max(e, __shfl_xor(e, o, 64));
+  return e;
+}
+constexpr int ROOM = 16;   // powers of two over the group's largest: |q8 . codes| 2^-ROOM 2^121 < 2^127
+
+// Codes with the power e, as the low byte of x 2^-e + 1.5 2^23, whose last place
+// is 1: the sum rounds to the nearest whole number, ties to even, in two's
+// complement.  `base`: the group's largest power.
+template <typename E, int NS> __device__ __forceinline__ void quantise(const RawQ<E, NS>& raw, int g, int e, int base, bool odd, Query<E, NS>& q) {
+  const float inv = ldexpf(1.f, -e);                    // a normal number: -126 <= e <= 121
+  const float sq = ldexpf(1.f, e - base - ROOM);
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -132,7 +153,7 @@ template <int NS> __device__ __forceinline__ void load_pages(const PageSelectArg
   if (!ok) p.sk = __builtin_nanf("");
 }
 
-// The products of a tile: v[j] = (q8 . codes) sq for row 4g + j and page n.
+// The products of a tile: v[j] = (q8 . codes) sq 2^-base-16 for row 4g + j and page n.
 // The page's scale is positive, so the maximum over heads may come before it.
 template <typename E, int NS> __device__ __forceinline__ void products(const Query<E, NS>& q, const Pages<NS>& p, float (&v)[4]) {
   i32x4 acc = {0, 0, 0, 0};
@@ -160,9 +181,19 @@ __device__ __forceinline__ void score_row(const PageSelectArgs& a, int r, int h,
   float* to = a.score + ((size_t)r * a.Hkv + h) * a.NB;
   const int step = 16 * PG * shares, first = 16 * PG * share;
   if (first >= nb) return;
+  const E* query = static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G) * D + 16 * g;
+  int base = -126;                                       // the group's largest power, of all its tiles
+  if (a.G > 16) {
+    for (int h0 = 0; h0 < a.G; h0 += 16) {
+      RawQ<E, NS> raw;
+      raw.load(query + (size_t)min(h0 + n, a.G - 1) * D);
+      bool odd;
+      base = max(base, group_max<16>(power_of(peak<E, NS>(raw, odd))));
+    }
+  }
   for (int h0 = 0; h0 < a.G; h0 += 16) {
     RawQ<E, NS> raw;                                     // heads beyond the group: the last one again
-    raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + min(h0 + n, a.G - 1)) * D + 16 * g);
+    raw.load(query + (size_t)min(h0 + n, a.G - 1) * D);
     int page[PG];
     auto look_up = [&](int p0) {
 #pragma unroll
@@ -176,8 +207,10 @@ __device__ __forceinline__ void score_row(const PageSelectArgs& a, int r, int h,
 #pragma unroll
     for (int u = 0; u < PG; ++u) load_pages<NS>(a, page[u], h, g, pg[u]);
     look_up(first + step);
+    bool odd;
+    const int e = power_of(peak<E, NS>(raw, odd));
     Query<E, NS> q;
-    quantise<E, NS>(raw, g, q);
+    quantise<E, NS>(raw, g, e, a.G > 16 ? base : group_max<16>(e), odd, q);
     for (int p0 = first; p0 < nb; p0 += step) {
       float x[PG], sk[PG];
 #pragma unroll
@@ -281,7 +314,9 @@ __global__ __launch_bounds__(64 * SW, sizeof(E) == 4 ? 2 : 4) void score_rows_ke
     const int r = min(row0 + t * TT + n / GP, a.R - 1), hd = min(n % GP, a.G - 1);
     RawQ<E, NS> raw;                                     // rows and heads beyond the last: the last again
     raw.load(static_cast<const E*>(a.q) + r * a.ldq + (size_t)(h * a.G + hd) * D + 16 * g);
-    quantise<E, NS>(raw, g, q[t]);
+    bool odd;
+    const int e = power_of(peak<E, NS>(raw, odd));
+    quantise<E, NS>(raw, g, e, group_max<GP>(e), odd, q[t]);
     if (sizeof(E) == 4) asm volatile("" ::: "memory");   // not all tiles' raw elements at once
   }
   while (true) {

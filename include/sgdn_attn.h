@@ -183,10 +183,13 @@ int sgdn_paged_attend_sparse(const sgdn_paged* p, const void* q, int64_t ldq, co
  * and the last n_local are always picked; the others are ranked by
  *     max over the group's query heads of  (q8 . codes_j) sq scale_j
  * with q8, sq the codes and the power of two of the query vector, formed as a
- * page summary's are (not finite elements count as 0).  The dot product is
- * exact in whole numbers and the powers of two leave it so, hence the score
- * and the choice do not depend on any order of evaluation; equal scores go
- * to the lower block, a score that is not a number ranks last.
+ * page summary's are (not finite elements count as 0).  The scores are exact
+ * and the choice does not depend on any order of evaluation; equal scores go
+ * to the lower block, a score that is not a number ranks last.  Exact is
+ * meant for scale_j up to 2^121, the largest that sgdn_paged_write makes, and
+ * for sq and sq scale_j of at least 2^-133 times the largest sq of the group's
+ * heads (always so where the heads' largest elements lie within 2^7 of each
+ * other); scores of a head or a summary below that are rounded in fp32.
  *   codes, scale of sgdn_paged_write
  *   blocks       [R, Hkv, n_blocks] out: min(n_blocks, nb) blocks in rising
  *                order, then -1
