@@ -594,12 +594,21 @@ def _row_view(t, name, device, dtype, shape):
     return ld if rows > 1 else heads * d
 
 
+def _int32(**sizes):
+    """The library's sizes are 32 bits wide; ctypes would take them modulo 2^32."""
+    for name, x in sizes.items():
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError(f"{name} must fit 32 bits, got {x}")
+
+
 @functools.lru_cache(maxsize=256)
 def _paged(rows, q_heads, cache_shape, dtype, out_dtype=None, batch=1, width=1, max_len=None):
     """The shape of a call, by its sizes (made once for each: small calls are bound by this side)."""
     n_pages, n_kv, page, d = cache_shape
     if max_len is not None and max_len < 1:
         raise ValueError(f"max_len must be positive (or None), got {max_len}")
+    _int32(rows=rows, batch=batch, query_heads=q_heads, heads=n_kv, d=d, page=page,
+           n_pages=n_pages, width=width, max_len=max_len or 0)
     code = _ocode(dtype)
     return Paged(rows, batch, q_heads, n_kv, d, page, n_pages, width,
                  0 if max_len is None else max_len, code,
@@ -608,6 +617,7 @@ def _paged(rows, q_heads, cache_shape, dtype, out_dtype=None, batch=1, width=1, 
 
 def paged_workspace_bytes(shape: Paged, n_blocks=0, select=False) -> int:
     """Workspace of paged_attend (``n_blocks`` 0), paged_attend_sparse or paged_select."""
+    _int32(n_blocks=n_blocks)
     return int(lib().sgdn_paged_workspace_bytes(ctypes.byref(shape), int(n_blocks), int(select)))
 
 
@@ -653,6 +663,8 @@ def paged_release(lens, done, table, free_list, free_pos, page, lens_out=None, f
     import torch
     dev, i32, i64 = lens.device, torch.int32, torch.int64
     B, W = _table_shape(table)
+    page = operator.index(page)
+    _int32(batch=B, width=W, page=page, free_list=free_list.numel())
     _paged_check(dev, ("lens", lens, i32, (B,)), ("done", done, torch.uint8, (B,)),
                  ("table", table, i32, None), ("free_list", free_list, i32, None),
                  ("free_pos", free_pos, i64, (2,)), ("lens_out", lens_out, i32, (B,)),
@@ -682,9 +694,10 @@ def paged_plan(lens, add, table, free_list, free_pos, page, rows, lens_out=None,
     import torch
     dev, i32, i64 = lens.device, torch.int32, torch.int64
     B, W = _table_shape(table)
-    rows = int(rows)
+    rows, page = int(rows), operator.index(page)
     if rows < 0:
         raise ValueError(f"rows must not be negative, got {rows}")
+    _int32(batch=B, width=W, page=page, rows=rows, free_list=free_list.numel())
     _paged_check(dev, ("lens", lens, i32, (B,)), ("add", add, i32, (B,)),
                  ("table", table, i32, None), ("free_list", free_list, i32, None),
                  ("free_pos", free_pos, i64, (2,)), ("lens_out", lens_out, i32, (B,)),
@@ -824,10 +837,12 @@ def paged_select(q, codes, code_scale, table, row_len, page, n_blocks, row_req=N
     if codes.dim() != 3:
         raise ValueError("codes must be [n_pages, Hkv, d]")
     n_pages, n_kv, d = codes.shape
+    page, n_blocks = operator.index(page), operator.index(n_blocks)
+    n_sink, n_local = operator.index(n_sink), operator.index(n_local)
+    _int32(n_blocks=n_blocks, n_sink=n_sink, n_local=n_local)
     ldq = _row_view(q, "q", dev, q.dtype, (None, None, d))
     rows = q.shape[0]
     B, W = _table_shape(table)
-    page, n_blocks = operator.index(page), operator.index(n_blocks)
     max_len = None if max_len is None else operator.index(max_len)
     if row_req is None and rows > B:
         raise ValueError("without row_req, row r is request r: more rows than requests")
