@@ -13,6 +13,7 @@ using namespace sgdn;
 constexpr size_t NO_WORKSPACE = 256;   // answer of sgdn_paged_workspace_bytes where none is used
 constexpr int MAX_LIST = 4096;     // blocks of a list
 constexpr int MAX_NB = 16384;      // blocks of a row that are ranked
+constexpr int MAX_COUNT = 0x7fffffff - 1024;   // requests, rows of a plan: counted in steps of up to 1024
 
 int log2_page(int page) {
   switch (page) {
@@ -149,6 +150,7 @@ int sgdn_paged_release(int32_t batch, int32_t page, int32_t width, int32_t n_fre
                        int64_t* free_pos_out, void* stream) {
   if (batch < 1 || page < 1 || width < 1 || n_free < 1) return SGDN_EINVAL;
   if (log2_page(page) < 0 || (int64_t)width * page >= (INT64_C(1) << 31)) return SGDN_EUNSUPPORTED;
+  if (batch > MAX_COUNT) return SGDN_EUNSUPPORTED;
   if (!lens || !done || !table || !free_list || !free_pos || !lens_out || !free_pos_out)
     return SGDN_EINVAL;
   const ReleaseArgs a{batch, page, width, n_free, lens, done, table, free_list, free_pos, lens_out, free_pos_out};
@@ -162,6 +164,7 @@ int sgdn_paged_plan(int32_t batch, int32_t page, int32_t width, int32_t rows, in
                     int32_t* row_req, int32_t* row_len, int32_t* status, void* stream) {
   if (batch < 1 || page < 1 || width < 1 || rows < 0 || n_free < 1) return SGDN_EINVAL;
   if (log2_page(page) < 0 || (int64_t)width * page >= (INT64_C(1) << 31)) return SGDN_EUNSUPPORTED;
+  if (batch > MAX_COUNT || rows > MAX_COUNT) return SGDN_EUNSUPPORTED;
   if (!lens || !add || !table || !free_list || !free_pos || !lens_out || !free_pos_out || !cu ||
       !page_cu || !status)
     return SGDN_EINVAL;

@@ -89,7 +89,8 @@ typedef struct {
  *                request order
  *   free_pos     [2] int64 in; free_pos_out [2] out, may be free_pos
  *   lens_out     [B] out, 0 for an ended request, lens otherwise; may be lens
- * A negative length gives nothing back; one beyond W P gives W pages. */
+ * A negative length gives nothing back; one beyond W P gives W pages.
+ * batch < 2^31 - 1024 (SGDN_EUNSUPPORTED otherwise). */
 int sgdn_paged_release(int32_t batch, int32_t page, int32_t width, int32_t n_free,
                        const int32_t* lens, const uint8_t* done, const int32_t* table,
                        int32_t* free_list, const int64_t* free_pos, int32_t* lens_out,
@@ -116,7 +117,8 @@ int sgdn_paged_release(int32_t batch, int32_t page, int32_t width, int32_t n_fre
  * question included, of those that are not refused for 2 or 8: a request
  * that needs pages is refused (1) if the sum of needed pages exceeds the
  * ring's, one that has rows is refused (4) if the sum of rows exceeds
- * `rows`.  The page numbers that the ring holds are taken as they are. */
+ * `rows`.  The page numbers that the ring holds are taken as they are.
+ * batch and rows < 2^31 - 1024 (SGDN_EUNSUPPORTED otherwise). */
 int sgdn_paged_plan(int32_t batch, int32_t page, int32_t width, int32_t rows, int32_t n_free,
                     const int32_t* lens, const int32_t* add, int32_t* table,
                     const int32_t* free_list, const int64_t* free_pos, int32_t* lens_out,

@@ -71,3 +71,21 @@ def test_refused_on_the_device():
             ops.paged_select(q, codes, scale, table, length, 16, 2, **kw)
     with pytest.raises(ValueError, match="page"):
         ops.paged_select(q, codes, scale, table, length, 2 ** 32 + 16, 2)
+
+
+def _fake_plan(batch, rows):
+    import ctypes
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    fake = [ctypes.c_void_p(0x1000)] * 13           # never dereferenced: refused, or no device here
+    L = ops.lib()
+    return (L.sgdn_paged_plan(batch, 16, 4, rows, 9, *fake, None), L.sgdn_paged_release(batch, 16, 4, 9, *fake[:7], None))
+
+
+@pytest.mark.parametrize("batch, rows", [(2 ** 31 - 1024, 5), (2 ** 31 - 1, 5), (5, 2 ** 31 - 1024), (5, 2 ** 31 - 1)])
+def test_bookkeeping_of_more_than_its_counters_hold(batch, rows):
+    """Kernels count requests and rows in steps of up to 1024: the last step has to end below 2^31."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("checks of arguments, on hosts without a device")
+    plan, release = _fake_plan(batch, rows)
+    assert plan == -2 and (release == -2) == (batch > 5)
