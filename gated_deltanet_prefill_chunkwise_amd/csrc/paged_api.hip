@@ -179,6 +179,7 @@ int sgdn_paged_write(const sgdn_paged* p, const void* k, const void* v, int64_t 
                      float* scale, void* stream) {
   const int st = check_shape(p);
   if (st != SGDN_OK) return st;
+  if (((int64_t)p->rows + 15) / 16 * 256 >= (INT64_C(1) << 32)) return SGDN_EUNSUPPORTED;   // threads: 16 rows a workgroup
   if ((codes == nullptr) != (scale == nullptr)) return SGDN_EINVAL;
   if (p->rows == 0) return SGDN_OK;
   if (!k || !v || !slot || !k_cache || !v_cache) return SGDN_EINVAL;

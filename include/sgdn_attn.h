@@ -61,9 +61,9 @@ extern "C" {
 
 /* Shape of a call.  Supported: D in {64, 128, 256}, P in {16, 32, 64, 128},
  * Hq a multiple of Hkv, W P < 2^31, n_pages P < 2^31, R Hq < 2^28, and
- * R Hkv ceil(Hq / (16 Hkv)) < 2^24 - 8 for the attention, R Hkv < 2^22 - 8 for
- * the choice of blocks (SGDN_EUNSUPPORTED otherwise; non-positive values are
- * SGDN_EINVAL, rows = 0 does nothing). */
+ * R < 2^28 - 15 for the write, R Hkv ceil(Hq / (16 Hkv)) < 2^24 - 8 for the
+ * attention, R Hkv < 2^22 - 8 for the choice of blocks (SGDN_EUNSUPPORTED
+ * otherwise; non-positive values are SGDN_EINVAL, rows = 0 does nothing). */
 typedef struct {
   int32_t rows;      /* R: rows of q (or k, v)                               */
   int32_t batch;     /* B: rows of the block table                           */

@@ -89,3 +89,17 @@ def test_bookkeeping_of_more_than_its_counters_hold(batch, rows):
         pytest.skip("checks of arguments, on hosts without a device")
     plan, release = _fake_plan(batch, rows)
     assert plan == -2 and (release == -2) == (batch > 5)
+
+
+def test_write_of_more_rows_than_a_launch_holds():
+    """16 rows a workgroup of 256: 2^28 - 15 rows and more would round up to 2^32 threads."""
+    import ctypes
+    import torch
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    if torch.cuda.is_available():
+        pytest.skip("checks of arguments, on hosts without a device")
+    fake = ctypes.c_void_p(0x1000)
+    for rows, status in ((2 ** 28 - 1, -2), (2 ** 28 - 15, -2), (2 ** 28 - 16, -1)):   # enough room: the next check
+        shape = ops.Paged(rows, 1, 1, 1, 64, 16, 100, 1, 0, 1, 1)
+        k = None if status == -1 else fake
+        assert ops.lib().sgdn_paged_write(ctypes.byref(shape), k, fake, 64, 64, fake, fake, fake, None, None, None) == status
