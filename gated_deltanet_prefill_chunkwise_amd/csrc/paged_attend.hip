@@ -27,8 +27,12 @@
 // largest weight.
 //
 // 16-bit weights enter the second product in two parts, the number rounded to
-// the type and what that left: the time of the first three calls below stays, and o
-// errs by its own rounding only.
+// the type and what that left, itself rounded: a weight errs by 2^-17 of itself
+// (bf16: a remainder of at most 2^-8, of which 8 bits are held) or 2^-23 (fp16,
+// and 2^-35 of the row's largest weight, as nothing lies below 2^-24), so o by
+// that part of sum p |v|.  Far under a 16-bit o's own rounding; an fp32 o of bf16
+// inputs is good to 2^-17, not to fp32.  The time of the first three calls below
+// stays what it is with one part.
 //
 // Bound: HBM, each key and value once per row.  (At most 16 of 16 columns of
 // the products are used; at 16 heads a group that is 4 flops a byte.)

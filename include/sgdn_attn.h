@@ -43,8 +43,11 @@
  *   them.  Products run on the matrix cores with fp32 accumulation; the
  *   softmax maximum, sum and the output accumulate in fp32.  With 16-bit
  *   inputs the softmax weights enter their product as two numbers of that type
- *   (weight and remainder), whichever kernel takes a row.  With fp32 inputs
- *   nothing is rounded below fp32.  A row's bits may depend on the lists of its
+ *   (weight and remainder), whichever kernel takes a row: beside fp32's
+ *   roundings and its own, o errs by at most 2^-17 (bf16) or 2^-23 (fp16, and
+ *   2^-35 of the largest weight for each key) of the weighted mean of |v|.  So
+ *   an fp32 o of bf16 inputs is good to 2^-17.  With fp32 inputs nothing is
+ *   rounded below fp32.  A row's bits may depend on the lists of its
  *   neighbours (sgdn_paged_attend_sparse of many rows: rows that share their
  *   lists are taken together, and sum in another order), its error bound not.
  * - Alignment: q, k, v, the caches, codes and o start at 16 bytes; row
