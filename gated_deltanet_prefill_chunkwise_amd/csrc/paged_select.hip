@@ -18,9 +18,12 @@
 //
 // Bound and measured: a decode step by latency (32 rows of 534 to 2048 pages of
 // 64, 32/8 heads of 128: 18.3 us for 45 MB of codes and scales, 1/128 of the
-// keys and values, then 11.6 to pick 64); prompts by vector instructions, a
-// maximum over heads and a store for each score that the products make (6378
-// rows of 4 requests, up to 256 pages, 16/2 of 256: 31 us, and 14 to pick 16).
+// keys and values, then 11.6 to pick 64).  Prompts (6378 rows of 4 requests, up to
+// 256 pages, 16/2 of 256: 31 us, and 14 to pick 16) by vector instructions first,
+// scales, a maximum over heads and a store for each score that the products make:
+// about half of the time (8192 rows, 1024 pages: 22.3 million of them, four
+// cycles each on 1024 SIMDs, are 36 of 74 us).  The other half, LDS reads, the
+// barrier of each stage of 32 pages and stores, has not been told apart.
 #include <type_traits>
 
 #include "common.h"
@@ -257,11 +260,12 @@ __global__ __launch_bounds__(64 * SW) void score_row_kernel(PageSelectArgs a, in
 // stages of 32 through registers into two LDS buffers, the next on its way.
 // (Read by each wave from global memory, a page's 16 bytes for each lane are an
 // access of the L1 each: 45 million for 8192 rows and 1024 pages of two heads,
-// 73 us of 99; now 74 us, with vector instructions in front.  4 tiles a wave:
-// 117, though fewer workgroups read the codes; 64 pages a stage and 8 waves: 67
-// there and no change below 4000 rows.)  Tokens of different requests are taken request by request,
-// and where they are more than a few (new tokens of other requests behind a
-// prompt), row by row, each wave its own.
+// 73 us of 99; now 74 us.  4 tiles a wave: 117, though fewer workgroups read the
+// codes; 64 pages a stage and 8 waves: 67 there and no change below 4000 rows.)
+// Tokens of different requests are taken request by request, and where they are
+// more than a few (new tokens of other requests behind a prompt), row by row,
+// each wave its own: 2048 and 100 such rows take 155 us in one call, 62 and 27
+// in two (32/8 heads of 128, 512 blocks).
 constexpr int QT = 2;      // 16-row tiles of a wave
 constexpr int SP = 32;     // pages of a stage
 
@@ -614,6 +618,8 @@ template <typename E, int D> hipError_t launch_score_d(const PageSelectArgs& a, 
   // each 55 and 19, 39 and 29, 37 and 36, 31 and 38, 39 and 104 us; 1 request
   // with 16, 64, 128 rows 14 and 12, 16 and 19, 18 and 26; 16/2 heads of 256: 16
   // with 16 each (1000 blocks) 20 and 35; 8/8 of 64: 64 with 8 each 87 and 46.
+  // (All requests of these had rows.  B counts the block table's: 2048 rows of one
+  // request take 39 us with its row alone for a table and 102 in a table of 512.)
   int gp = 1;
   while (gp < a.G) gp <<= 1;
   if ((int64_t)a.R * gp >= 32 * (int64_t)a.B && (int64_t)a.R * a.Hkv * D >= 1 << 16 && a.G <= 16) {

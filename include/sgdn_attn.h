@@ -50,6 +50,12 @@
  *   rounded below fp32.  A row's bits may depend on the lists of its
  *   neighbours (sgdn_paged_attend_sparse of many rows: rows that share their
  *   lists are taken together, and sum in another order), its error bound not.
+ * - A call's work is laid out from its shape, before the device knows any
+ *   length.  max_len as the step needs it, tables without empty rows and lists
+ *   no longer than the rows fill are therefore faster; so are a call of its
+ *   own for a row that sees far more than the others, and for the prompts of a
+ *   step that has single rows too.  Rows of one request read its context once
+ *   each in sgdn_paged_attend.
  * - Alignment: q, k, v, the caches, codes and o start at 16 bytes; row
  *   strides are multiples of 16 bytes.  Otherwise SGDN_EINVAL.
  */
