@@ -320,10 +320,13 @@ __device__ __forceinline__ void attend_unit(const PageAttendArgs& a, int unit, i
 
 // Rows next to each other (SPARSE) and the head tiles of a group read the same
 // pages: with one split each XCD (workgroup id mod 8) gets one run of the units.
-// With several, of few units, a unit's workgroups lie on different XCDs.  Kept
-// together, the splits outermost in the grid, they leave XCDs without work: one
-// row of 32768 tokens, 64/2 heads of 128 24.2 us and not 15.8, 128/1 27.6 and
-// 19.7; sparse steps of 2 to 16 splits the same within 2%.
+// With S splits a workgroup's XCD is (unit' S + split) mod 8, unit' the number
+// before it is permuted: for S a multiple of 8, few units, the same split of
+// every unit, so that head tiles meet there as well; for other S units and splits
+// are spread.  The splits outermost in the grid, a unit's on one XCD, part the head
+// tiles of 8 units or fewer: one row of 32768 tokens, 64/2 heads of 128 24.2 us
+// and not 15.8, 128/1 27.6 and 19.7; sparse steps of 2 to 16 splits the same
+// within 2%.
 __device__ __forceinline__ int unit_of_xcd(int i, int units) { return (i & 7) * ((units + 7) >> 3) + (i >> 3); }
 
 template <typename E, typename O, int D, bool SPARSE>
@@ -344,8 +347,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(E) == 2 ? 2 : 1) void attend_kernel
 // rows of 16 of 256 blocks, a workgroup a row and so (tiles with weights in one
 // part): 171 and 146 us (32/8 heads of 128, nothing left), 160 and 155 (16/2 of
 // 256); 1208 and 1247, 715 and 761 where every row is left, as the work is dealt
-// out ahead.  (D = 256: one wave
-// a SIMD, as two leave too few registers for the loop.)
+// out ahead.  (D = 256: one wave a SIMD, as two leave too few registers for the
+// loop.)
 template <typename E, typename O, int D>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void left_kernel(PageAttendArgs a, int units) {
   __shared__ Joined<D> lds;
