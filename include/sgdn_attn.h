@@ -47,9 +47,10 @@
  *   roundings and its own, o errs by at most 2^-17 (bf16) or 2^-23 (fp16, and
  *   2^-35 of the largest weight for each key) of the weighted mean of |v|.  So
  *   an fp32 o of bf16 inputs is good to 2^-17.  With fp32 inputs nothing is
- *   rounded below fp32.  A row's bits may depend on the lists of its
- *   neighbours (sgdn_paged_attend_sparse of many rows: rows that share their
- *   lists are taken together, and sum in another order), its error bound not.
+ *   rounded below fp32.  A row's bits may depend on its neighbours' lists and
+ *   on values in them that are not finite (sgdn_paged_attend_sparse of many
+ *   rows: rows that share their lists are taken together, and sum in another
+ *   order), its error bound not.
  * - A call's work is laid out from its shape, before the device knows any
  *   length.  max_len as the step needs it, tables without empty rows and lists
  *   no longer than the rows fill are therefore faster; so are a call of its
