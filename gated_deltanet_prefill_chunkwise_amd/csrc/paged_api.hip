@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "../../include/sgdn_attn.h"
+#include "check.h"
 #include "paged.h"
 
 namespace {
@@ -15,64 +16,13 @@ constexpr int MAX_LIST = 4096;     // blocks of a list
 constexpr int MAX_NB = 16384;      // blocks of a row that are ranked
 constexpr int MAX_COUNT = 0x7fffffff - 1024;   // requests, rows of a plan: counted in steps of up to 1024
 
-int log2_page(int page) {
-  switch (page) {
-    case 16: return 4;
-    case 32: return 5;
-    case 64: return 6;
-    case 128: return 7;
-    default: return -1;
-  }
-}
-
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
-
-// A row stride: at least the row, and a multiple of 16 bytes.
-bool bad_stride(int64_t ld, int64_t row, int dtype) {
-  const int64_t esz = dtype == SGDN_F32 ? 4 : 2;
-  return ld < row || (ld * esz) % 16 != 0 || ld > (INT64_C(1) << 40);
-}
-
-// The fields every call uses.
-int check_shape(const sgdn_paged* p) {
-  if (p == nullptr) return SGDN_EINVAL;
-  if (p->rows < 0 || p->n_q < 1 || p->n_kv < 1 || p->d < 1 || p->page < 1 || p->n_pages < 1)
-    return SGDN_EINVAL;
-  if (p->dtype != SGDN_F32 && p->dtype != SGDN_BF16 && p->dtype != SGDN_F16) return SGDN_EINVAL;
-  if (p->d != 64 && p->d != 128 && p->d != 256) return SGDN_EUNSUPPORTED;
-  if (log2_page(p->page) < 0) return SGDN_EUNSUPPORTED;
-  if (p->n_q % p->n_kv != 0) return SGDN_EUNSUPPORTED;
-  if (p->n_kv > 65535) return SGDN_EUNSUPPORTED;                     // a grid dimension
-  if ((int64_t)p->rows * p->n_q >= (INT64_C(1) << 28)) return SGDN_EUNSUPPORTED;
-  if ((int64_t)p->n_pages * p->page >= (INT64_C(1) << 31)) return SGDN_EUNSUPPORTED;
-  return SGDN_OK;
-}
-
-// ... and those of the calls that read a block table.
-int check_read(const sgdn_paged* p) {
-  const int st = check_shape(p);
-  if (st != SGDN_OK) return st;
-  if (p->batch < 1 || p->width < 1 || p->max_len < 0) return SGDN_EINVAL;
-  if ((int64_t)p->width * p->page >= (INT64_C(1) << 31)) return SGDN_EUNSUPPORTED;
-  if (p->max_len > p->width * p->page) return SGDN_EINVAL;
-  return SGDN_OK;
-}
-
-// A launch holds fewer than 2^32 threads: `groups` workgroups, in eighths of
-// the chip, of `threads`.
-bool too_many(int64_t groups, int threads) { return (groups + 7) / 8 * 8 * threads >= (INT64_C(1) << 32); }
-
 // Rows, heads and head tiles of the attention: a workgroup of 256 each.
 bool too_many_units(const sgdn_paged* p) {
   return too_many((int64_t)p->rows * p->n_kv * ((p->n_q / p->n_kv + 15) / 16), 256);
 }
 
-int longest(const sgdn_paged* p) { return p->max_len > 0 ? p->max_len : p->width * p->page; }
-
 // Rows and heads of the choice: a workgroup of up to 1024 each.
 bool too_many_picks(const sgdn_paged* p) { return too_many((int64_t)p->rows * p->n_kv, 1024); }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct AttendPlan { int S, MT, TQ; size_t off_ml, total; };
 

@@ -1,0 +1,56 @@
+// Launch interfaces of the kernels around the paged cache (internal to
+// libsgdn.so).  Notation as in include/sgdn_serve.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace sgdn {
+
+struct HeadsArg { const void* in; void* out; int64_t in_row, in_head, out_row, out_head; };
+
+struct RopeArgs {
+  HeadsArg q, k;
+  int R, Hq, Hk, D, rot;
+  const int32_t* pos;
+  int pos_offset;
+  const double* freqs;
+  float magnitude;
+  const void* wq;            // NULL: zeros
+  const void* wk;
+  float w_offset, eps;
+  int slices;                // of a row's heads, a wave each
+};
+
+// A tile of the chunk attention: rows row0 .. row0 + rows - 1 of request req
+// (-1: of none).
+struct ChunkTile { int32_t row0, rows, req, pad; };
+
+struct ChunkArgs {
+  const void* q;
+  int64_t ldq;
+  const void* kc;
+  const void* vc;
+  const int32_t* table;
+  const int32_t* cu;
+  const int32_t* lens;
+  void* o;
+  float* lse;                // NULL: not wanted
+  int32_t* count;            // [1] tiles
+  ChunkTile* tiles;          // [cap]
+  int R, B, Hq, Hkv, G, lp, n_pages, W, max_len;
+  int TR, GT, MT;            // rows of a tile, query heads of one, head tiles of a group
+  int cap;                   // tiles at most
+  float scale;               // of the scores, times log2(e)
+};
+
+// dtype: the boundary's sgdn_dtype values (0 fp32, 1 bf16, 2 fp16)
+int rope_slices(int R, int heads, int d, int dtype);
+hipError_t launch_rope(const RopeArgs& a, int dtype, int w_dtype, bool norm, bool interleaved, hipStream_t s);
+
+// Columns ((row, query head) pairs of one key/value head) of a tile.
+int chunk_columns(int dtype, int d);
+hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
+
+}  // namespace sgdn

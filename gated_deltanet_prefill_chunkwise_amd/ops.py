@@ -1,5 +1,6 @@
-"""Thin Python binding of libsgdn.so (C ABI in include/sgdn.h and, for the
-paged attention operators ``paged_*``, include/sgdn_attn.h).
+"""Thin Python binding of libsgdn.so (C ABI in include/sgdn.h, for the paged
+attention operators ``paged_*`` include/sgdn_attn.h, and for what stands around
+them, ``rope*``, ``norm_rope`` and ``paged_attend_chunk``, include/sgdn_serve.h).
 
 Argument marshalling only: every step of the prefill runs in the library's HIP
 kernels.  Tensors are torch device tensors (torch provides memory and the
@@ -22,7 +23,9 @@ EXPORTS = ("sgdn_workspace_bytes", "sgdn_event_capacity", "sgdn_prefill_dense", 
            "sgdn_select_noalloc",
            "sgdn_paged_release", "sgdn_paged_plan", "sgdn_paged_write",
            "sgdn_paged_workspace_bytes", "sgdn_paged_attend", "sgdn_paged_attend_sparse",
-           "sgdn_paged_select")
+           "sgdn_paged_select",
+           "sgdn_rope_freqs", "sgdn_rope", "sgdn_norm_rope", "sgdn_paged_chunk_workspace_bytes",
+           "sgdn_paged_attend_chunk")
 NOALLOC_SCRATCH_BYTES = 4 << 20   # SGDN_NOALLOC_SCRATCH_BYTES
 
 
@@ -63,6 +66,16 @@ NF_INPUT = {"q": 1, "k": 2, "v": 4, "a": 8, "beta": 16, "z": 32, "s0": 64}
 NF_OUTPUT = {"o": 1, "s_final": 2}
 STAT_FIELDS = ("E", "E_max", "n_low", "n_medium", "n_high", "k_low", "k_medium", "k_high",
                "n_snapshots", "nonfinite_input", "nonfinite_output")
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class RopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "n_q", "n_k", "d", "rot", "layout", "dtype", "w_dtype")] + \
+               [(n, Strides) for n in ("q", "k", "q_out", "k_out")]
 
 
 class Debug(ctypes.Structure):
@@ -128,6 +141,16 @@ def lib():
                                         vp]
         for name in ("release", "plan", "write", "attend", "attend_sparse", "select"):
             getattr(L, "sgdn_paged_" + name).restype = i32
+        RS, f64 = ctypes.POINTER(RopeShape), ctypes.c_double
+        L.sgdn_rope_freqs.argtypes = [i32, i32, f64, f64, f64, f64, f64, vp, vp]
+        L.sgdn_rope.argtypes = [RS, vp, vp, vp, i32, vp, f64, vp, vp, vp]
+        L.sgdn_norm_rope.argtypes = [RS, vp, vp, vp, vp, f32, f32, vp, i32, vp, f64, vp, vp, vp]
+        L.sgdn_paged_chunk_workspace_bytes.argtypes = [PG]
+        L.sgdn_paged_chunk_workspace_bytes.restype = sz
+        L.sgdn_paged_attend_chunk.argtypes = [PG, vp, i64, vp, vp, vp, vp, vp, f32, vp, vp, vp, sz,
+                                              vp]
+        for name in ("rope_freqs", "rope", "norm_rope", "paged_attend_chunk"):
+            getattr(L, "sgdn_" + name).restype = i32
         L.sgdn_status_string.argtypes = [i32]
         L.sgdn_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -862,3 +885,191 @@ def paged_select(q, codes, code_scale, table, row_len, page, n_blocks, row_req=N
             n_blocks, n_sink, n_local, blocks.data_ptr(), ws, nbytes,
             hold=(q, codes, code_scale, table, row_req, row_len, blocks, held))
     return blocks
+
+
+# --- What stands around the paged cache (include/sgdn_serve.h) ---------------
+# Streams and devices as above.
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_pair": 3, "by_turns": 4}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _choice(name, value, choices):
+    if value not in choices:
+        raise ValueError(f"{name} must be one of {', '.join(choices)}, got {value!r}")
+    return choices[value]
+
+
+def rope_freqs(rot, base=10000.0, scaling="plain", factor=1.0, original=0, low=1.0, high=32.0,
+               device=None):
+    """Frequencies of the ``rot / 2`` pairs (fp64, radians per token) and the
+    magnitude that goes with them, for ``rope`` and ``norm_rope``.
+
+    ``scaling``: "plain"; for contexts stretched by ``factor`` "linear", "base",
+    "by_pair" or "by_turns" (the last two: pairs that turn more than ``high``
+    times in ``original`` tokens stay, those under ``low`` are slowed, those
+    between in part, by their number or by their turns).  Computed on the host;
+    with ``device`` the frequencies are copied there.
+    """
+    import torch
+    rot = operator.index(rot)
+    _int32(rot=rot)
+    freqs = torch.empty(max(rot // 2, 0), dtype=torch.float64)
+    magnitude = ctypes.c_double()
+    st = lib().sgdn_rope_freqs(rot, _choice("scaling", scaling, ROPE_SCALINGS), float(base),
+                               float(factor), float(original), float(low), float(high),
+                               freqs.data_ptr(), ctypes.addressof(magnitude))
+    if st != 0:
+        raise SgdnError(st, "sgdn_rope_freqs")
+    return (freqs if device is None else freqs.to(device)), magnitude.value
+
+
+def _heads_view(t, name, device, dtype, shape):
+    """[R, H, d] whose heads are contiguous: its row and head strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    row, head, e = t.stride()
+    if e != 1 and t.shape[2] > 1:
+        raise ValueError(f"each head of {name} must be contiguous, got strides {t.stride()}")
+    return row, head
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_shape(rows, n_q, n_k, d, rot, layout, dtype, w_dtype, *strides):
+    _int32(rows=rows, n_q=n_q, n_k=n_k, d=d, rot=rot)
+    return RopeShape(rows, n_q, n_k, d, rot, _choice("layout", layout, ROPE_LAYOUTS),
+                     _ocode(dtype), _ocode(w_dtype), *(Strides(*s) for s in strides))
+
+
+def _rope(name, q, k, weights, numbers, pos, freqs, layout, magnitude, pos_offset, q_out, k_out,
+          stream):
+    import torch
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("q or k must be given")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    if x.dim() != 3:
+        raise ValueError(f"q and k must have three dimensions, got {tuple(x.shape)}")
+    dev, dt = x.device, x.dtype
+    rows, _, d = x.shape
+    pos_offset = operator.index(pos_offset)
+    _int32(pos_offset=pos_offset)
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs must be [rot / 2], got {tuple(freqs.shape)}")
+    w_dtype = torch.float32
+    for w in weights:
+        if w is not None:
+            w_dtype = w.dtype
+    _paged_check(dev, ("pos", pos, torch.int32, (rows,)), ("freqs", freqs, torch.float64, None),
+                 *((n, w, w_dtype, (d,)) for n, w in zip(("q_weight", "k_weight"), weights)))
+    on = _On(dev, stream)
+    strides, n, outs = [], [], []
+    for what, t, out in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            n.append(0)
+            outs.append(None)
+            strides += [(0, 0), (0, 0)]
+            continue
+        s = _heads_view(t, what, dev, dt, (rows, None, d))
+        if out is None:
+            out = on.empty(t.shape, dt)
+        strides += [s, _heads_view(out, what + "_out", dev, dt, tuple(t.shape))]
+        n.append(t.shape[1])
+        outs.append(out)
+    shape = _rope_shape(rows, n[0], n[1], d, 2 * freqs.numel(), layout, dt, w_dtype,
+                        strides[0], strides[2], strides[1], strides[3])
+    on.call(name, ctypes.byref(shape), _optional(q), _optional(k), *numbers, pos.data_ptr(),
+            pos_offset, freqs.data_ptr(), float(magnitude), _optional(outs[0]), _optional(outs[1]),
+            hold=(q, k, *weights, pos, freqs, *outs))
+    return tuple(outs)
+
+
+def rope(q, k, pos, freqs, layout="half", magnitude=1.0, pos_offset=0, q_out=None, k_out=None,
+         stream=None):
+    """Rotary positions of queries [R, Hq, d] and keys [R, Hk, d] (either may be
+    None); returns (q, k).
+
+    Row r stands at ``pos[r] + pos_offset``; a negative place leaves the row out
+    (its outputs are not written), so that ``paged_plan``'s ``row_len`` can be
+    given with ``pos_offset`` -1.  The first 2 ``freqs.numel()`` elements of each
+    head are turned (``rope_freqs`` makes the frequencies and the magnitude),
+    the rest is copied.  ``layout``: pairs (i, i + rot/2) ("half") or
+    (2i, 2i + 1) ("interleaved").  q and k may be strided views whose heads are
+    contiguous; ``q_out`` and ``k_out`` may be q and k themselves.
+    """
+    return _rope("sgdn_rope", q, k, (), (), pos, freqs, layout, magnitude, pos_offset, q_out,
+                 k_out, stream)
+
+
+def norm_rope(q, k, q_weight, k_weight, pos, freqs, layout="half", magnitude=1.0, eps=1e-6,
+              weight_offset=0.0, pos_offset=0, q_out=None, k_out=None, stream=None):
+    """``rope`` of heads that are normed first: x / sqrt(mean x^2 + eps) times
+    (weight + ``weight_offset``), weights [d] of one type (None: zeros)."""
+    weights = (q_weight, k_weight)
+    return _rope("sgdn_norm_rope", q, k, weights,
+                 (_optional(q_weight), _optional(k_weight), float(weight_offset), float(eps)), pos,
+                 freqs, layout, magnitude, pos_offset, q_out, k_out, stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _chunk_bytes(*sizes):
+    return paged_chunk_workspace_bytes(_paged(*sizes))
+
+
+def paged_chunk_workspace_bytes(shape: Paged) -> int:
+    """Workspace of paged_attend_chunk."""
+    return int(lib().sgdn_paged_chunk_workspace_bytes(ctypes.byref(shape)))
+
+
+def paged_attend_chunk(q, k_cache, v_cache, table, cu, lens, scale=None, max_len=None, o=None,
+                       out_dtype=None, want_lse=False, lse=None, workspace=None, stream=None):
+    """``paged_attend`` for steps in which requests have many new tokens; returns (o, lse).
+
+    Rows ``cu[b]`` .. ``cu[b + 1] - 1`` are the last tokens of request b, which
+    has ``lens[b]`` with them (``cu`` and ``lens`` of ``paged_plan``): each sees
+    the tokens up to its own.  Rows of no request give 0 (lse -inf).  The other
+    arguments are those of ``paged_attend``.
+    """
+    import torch
+    dev, dt, i32 = k_cache.device, k_cache.dtype, torch.int32
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [n_pages, Hkv, page, d]")
+    d = k_cache.shape[3]
+    ldq = _row_view(q, "q", dev, dt, (None, None, d))
+    rows, n_q, _ = q.shape
+    B, W = _table_shape(table)
+    max_len = None if max_len is None else operator.index(max_len)
+    if o is not None:
+        out_dtype = o.dtype
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    _paged_check(dev, ("k_cache", k_cache, None, None), ("v_cache", v_cache, dt, k_cache.shape),
+                 ("table", table, i32, None), ("cu", cu, i32, (B + 1,)), ("lens", lens, i32, (B,)),
+                 ("o", o, None, (rows, n_q, d)), ("lse", lse, torch.float32, (rows, n_q)),
+                 ("workspace", workspace, None, None))
+    sizes = (rows, n_q, k_cache.shape, dt, out_dtype, B, W, max_len)
+    shape = _paged(*sizes)
+    on = _On(dev, stream)
+    nbytes = _chunk_bytes(*sizes)
+    if nbytes == 0:
+        raise SgdnError(-2, "sgdn_paged_chunk_workspace_bytes")
+    if workspace is None:
+        workspace = on.empty(nbytes, torch.uint8)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    if o is None:
+        o = on.empty((rows, n_q, d), out_dtype)
+    if want_lse and lse is None:
+        lse = on.empty((rows, n_q), torch.float32)
+    on.call("sgdn_paged_attend_chunk", ctypes.byref(shape), q.data_ptr(), ldq, k_cache.data_ptr(),
+            v_cache.data_ptr(), table.data_ptr(), cu.data_ptr(), lens.data_ptr(),
+            d ** -0.5 if scale is None else float(scale), o.data_ptr(), _optional(lse),
+            workspace.data_ptr(), nbytes,
+            hold=(q, k_cache, v_cache, table, cu, lens, o, lse, workspace))
+    return o, lse

@@ -22,6 +22,7 @@ Modules
            event layout (Eqs. 9-16)
   paged    paged softmax attention beside the linear layers: page bookkeeping,
            cache write and page summaries, attention, block choice
+  serve    rotary positions, norms of heads, attention of chunks around it
   sparse   deferred W, event-sparse H, two-chunk grouped O, end-to-end sparse
            prefill (Eqs. 15, 17-25)
 
@@ -33,4 +34,4 @@ invariants, and the end-to-end sparse outputs are pinned through the
 all-events-kept fixed point and the Eq. (25) identity.
 """
 
-from . import detfp, gdn, paged, selector, sparse  # noqa: F401
+from . import detfp, gdn, paged, selector, serve, sparse  # noqa: F401
