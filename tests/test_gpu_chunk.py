@@ -280,7 +280,7 @@ def test_binding_refusals():
                dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))):
         with pytest.raises(ValueError):
             call(**kw)
-    for kw, status in ((dict(max_len=1 << 20), -1), (dict(scale=float("inf")), -1), (dict(q=c.g(np.zeros((rows, 3, 64)))), -2)):
+    for kw, status in ((dict(max_len=1 << 20), -2), (dict(scale=float("inf")), -1), (dict(q=c.g(np.zeros((rows, 3, 64)))), -2)):
         with pytest.raises(ops.SgdnError) as e:
             call(**kw)
         assert e.value.status == status
