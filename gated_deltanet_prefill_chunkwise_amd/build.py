@@ -23,11 +23,14 @@ BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "intra.hip", "hscan.hip", "ochunk.hip", "misc.hip", "select.hip",
            "decode.hip", "paged_api.hip", "paged_plan.hip", "paged_write.hip", "paged_attend.hip",
-           "paged_select.hip", "paged_tiles.hip", "serve_api.hip", "rope.hip", "chunk.hip"]
+           "paged_select.hip", "paged_tiles.hip", "serve_api.hip", "rope.hip", "chunk.hip",
+           "chunk16.hip"]
 # hscan: products accumulate in ordinary vector registers (its state tiles are
-# also scaled and converted by vector instructions every event)
+# also scaled and converted by vector instructions every event); chunk16:
+# likewise, its scores
 EXTRA = {"select.hip": ["-ffp-contract=off"],
-         "hscan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+         "hscan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "chunk16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def hipcc() -> str:

@@ -1,0 +1,360 @@
+// Attention of chunks over a paged cache, 16-bit types (plan, join and the
+// formulas: chunk.hip).
+//
+// A workgroup takes 128 columns, 32 a wave, and walks the keys in blocks of 64
+// that lie in LDS, the next block on its way while this one is used.  Both
+// products run transposed with 32 x 32 x 16 matrix instructions:
+//   S^T [64 keys x 32 columns] = K Q^T: lane l = 32 f + n holds, of column n and of
+//     each 32 keys, keys 8 i + 4 f + j (i, j = 0 .. 3);
+//   A^T [D x 32 columns] += V^T P^T: the B operand of 16 keys takes eight of a
+//     lane's weights as they stand, keys 4 f + j and 8 + 4 f + j, and V^T comes
+//     in that order by two transposing reads.
+// So nothing crosses lanes between the products, and the running maximum, which
+// moves only where a score exceeds it by a threshold, is rarely shared.
+#include "chunk.h"
+
+namespace sgdn {
+
+namespace {
+
+constexpr int KB = CHUNK_KEYS, COLS = CHUNK16_COLS, NW = 4;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mma32(const bf16x8& a, const bf16x8& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(const fp16x8& a, const fp16x8& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// Two numbers rounded to E in a word, and each of them.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <typename E> __device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef E e2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, e2));
+}
+template <typename E> __device__ __forceinline__ float low(uint32_t w) {
+  if constexpr (__is_same(E, bf16)) return __builtin_bit_cast(float, w << 16);
+  else return to_f(__builtin_bit_cast(fp16, (uint16_t)w));
+}
+template <typename E> __device__ __forceinline__ float high(uint32_t w) {
+  if constexpr (__is_same(E, bf16)) return __builtin_bit_cast(float, w & 0xFFFF0000u);
+  else return to_f(__builtin_bit_cast(fp16, (uint16_t)(w >> 16)));
+}
+
+// 16-byte units of a row are permuted by the key's number, so that rows that are
+// read at once lie in different banks: unit u of key k is stored at u ^ f(k).
+// K is read 16 rows at once, one unit of each; V 4 or 8 rows, 64 or 32 bytes of each.
+template <int D> __device__ __forceinline__ int k_swap(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
+template <int D> __device__ __forceinline__ int v_swap(int key) {
+  return D == 64 ? ((key & 2) << 1) | ((key & 4) >> 1) : ((key & 3) << 2) | ((key & 4) >> 1);
+}
+
+// 16 bytes a lane from global memory to LDS (lane l to byte 16 l from `lds`).  In
+// asm, so that the compiler does not let every read of LDS wait for it: the
+// kernel waits itself, before the barrier in front of the block's first use.
+__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+}
+
+template <typename E, typename O, int D, int PARTS>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(ChunkArgs a) {
+  constexpr int NS = D / 16, DT = D / 32;            // reduction steps of the scores, 32-element tiles of an output
+  constexpr int U = D / 8, RPI = 64 / U, NI = 16 / RPI;   // units of a row, rows of a copy, copies of 16 keys
+  constexpr int TILE = KB * D;                       // elements of a block of keys
+  constexpr float BIAS = __is_same(E, fp16) ? 10.f : 0.f;   // see paged_attend.hip
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  E* const kbuf = reinterpret_cast<E*>(lds);         // two blocks of keys, then two of values
+  E* const vbuf = kbuf + 2 * TILE;
+
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, f = lane >> 5;
+  const int heads = a.Hkv * a.MT;
+  const int slot = blockIdx.x / heads, hm = blockIdx.x - slot * heads, h = hm / a.MT, mt = hm - h * a.MT;
+  const int head0 = h * a.G + mt * a.GT, gt = min(a.GT, a.G - mt * a.GT);
+  const int P = 1 << a.lp;
+  const E* kc = static_cast<const E*>(a.kc);
+  const E* vc = static_cast<const E*>(a.vc);
+
+  // byte offsets of this lane's part of the copies, from the first of 16 keys
+  uint32_t k_off[NI], v_off[NI];
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int key = j * RPI + lane / U, u = lane % U;
+    k_off[j] = (key * U + (u ^ k_swap<D>(key))) * 16;
+    v_off[j] = (key * U + (u ^ v_swap<D>(key))) * 16;
+  }
+  // elements at which this lane's reads of a block begin
+  int k_at[NS], v_at[DT < 4 ? DT : 4];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) k_at[s] = n * D + 8 * ((2 * s + f) ^ k_swap<D>(n));
+  const int m = lane & 15, v_key = 4 * f + (m >> 2);
+#pragma unroll
+  for (int d = 0; d < (DT < 4 ? DT : 4); ++d)
+    v_at[d] = v_key * D + 8 * ((4 * d + 2 * ((lane >> 4) & 1) + ((m & 3) >> 1)) ^ v_swap<D>(v_key)) + 4 * (m & 1);
+
+  const int64_t share = a.head->share, begin = slot * share, end = begin + share;
+  const int tiles = a.head->tiles;
+  for (int ti = a.start[slot]; ti < tiles; ++ti) {
+    const ChunkTile t = a.tiles[ti];
+    if (t.at >= end) break;
+    if (t.rows <= 0) continue;
+    const ChunkPart part = chunk_part(t, begin, end);
+    const int col = 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
+    const bool real = my_row < t.rows && my_head < gt;
+    const int row = t.row0 + min(my_row, t.rows - 1), head = head0 + min(my_head, gt - 1);
+    // columns that are none see what their row does: they change nothing
+    const int len = chunk_sees(a, t, row);
+    const int len_lo = __builtin_amdgcn_readlane(len, 0), len_hi = __builtin_amdgcn_readlane(len, 31);
+    const bool active = 32 * wave < t.rows * a.GT;
+    const int32_t* table = a.table + (size_t)max(t.req, 0) * a.W;
+
+    frag_t<E> qf[NS];
+    {
+      const E* q = static_cast<const E*>(a.q) + row * a.ldq + (size_t)head * D + 8 * f;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) qf[s] = ld8(q + 16 * s);
+    }
+    // A negative scale turns the query's sign, so that the largest product is the largest score.
+    // A scale of 0 goes into the query whole, as 0 times a masked score is no score.
+    if (a.scale <= 0.f) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qf[s][e] = a.scale == 0.f ? from_f<E>(0.f) : -qf[s][e];
+    }
+    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
+    float c = -INFINITY, l = 0.f;
+    bool seen = false;
+    f32x16 acc[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] = zero16();
+
+    // Lane l looks up the page of 16 keys number l of the next 16 blocks, -1 for none.
+    const int groups = (int)(((int64_t)t.longest + 15) >> 4);
+    int pages = -1;
+    auto look_up = [&](int block) {
+      const int g = 4 * block + lane;
+      int x = -1;
+      if (g < groups) x = table[(int)(((int64_t)g << 4) >> a.lp)];
+      pages = x >= 0 && x < a.n_pages ? x : -1;
+    };
+    // Wave w copies 16 keys number w of a block.
+    auto copy = [&](int block, int buf) {
+      const int g = 4 * block + wave;
+      const int page = max(__builtin_amdgcn_readlane(pages, g & 63), 0);      // a place that can be read
+      const size_t from = ((size_t)page * a.Hkv + h) * P + (((int64_t)g << 4) & (P - 1));
+      const E* k = kc + from * D;
+      const E* v = vc + from * D;
+      const uint32_t to = lds0 + (uint32_t)(buf * TILE + wave * 16 * D) * 2;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) copy_to_lds(k, k_off[j], to + j * 1024);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) copy_to_lds(v, v_off[j], to + 2 * TILE * 2 + j * 1024);
+    };
+
+    if (part.b0 < part.b1) {
+      look_up(part.b0 & ~15);
+      lds_barrier();                                   // the last tile's blocks have been read
+      copy(part.b0, 0);
+    }
+    for (int b = part.b0; b < part.b1; ++b) {
+      const int buf = (b - part.b0) & 1;
+      const uint64_t there = __ballot(pages >= 0);
+      const uint32_t valid = (uint32_t)(there >> ((4 * b) & 63)) & 15u;       // of this block's 16 keys each
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      lds_barrier();                                   // this block is whole, the other buffer free
+      if (b + 1 < part.b1) {
+        if (((b + 1) & 15) == 0) look_up(b + 1);
+        copy(b + 1, buf ^ 1);
+      }
+      const int key0 = b * KB;
+      // Places behind the last token and pages that are none may hold anything.
+      if (valid != 15u || key0 + KB > t.longest) {
+        for (int i = tid; i < TILE / 8; i += 64 * NW) {
+          const int key = i / U;
+          if (!((valid >> (key >> 4)) & 1u) || key0 + key >= t.longest) stv(vbuf + buf * TILE + 8 * i, zv());
+        }
+        lds_barrier();
+      }
+      if (!active || key0 >= len_hi) continue;
+      const bool full = valid == 15u && key0 + KB <= len_lo;
+
+      f32x16 s[2];
+      s[0] = zero16();
+      s[1] = zero16();
+      const E* kb = kbuf + buf * TILE;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const frag_t<E> k0 = ld8(kb + k_at[i]), k1 = ld8(kb + k_at[i] + 32 * D);
+        s[0] = mma32(k0, qf[i], s[0]);
+        s[1] = mma32(k1, qf[i], s[1]);
+      }
+      // Of 16 keys number g this lane's column sees key 8 i + 4 f + j (i = 0, 1) where 8 i + j < left(g).
+      auto left = [&](int g) { return (valid >> g) & 1u ? len - key0 - 16 * g - 4 * f : 0; };
+      if (!full) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int x = left(g);
+          seen = seen || x > 0;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (8 * (r >> 2) + (r & 3) >= x) s[g >> 1][8 * (g & 1) + r] = -INFINITY;
+        }
+      } else {
+        seen = true;
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
+      mx *= scale;                                     // its sign is in q
+      if (__ballot(mx > c + (BIAS + 4.f)) != 0ull) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        const float cn = fmaxf(c, mx - BIAS);
+        const float g = cn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(c - cn);
+        c = cn;
+        l *= g;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] *= g;
+      }
+      const float cs = c == -INFINITY ? 0.f : c;
+      frag_t<E> ph[4], pl[4];                          // of 16 keys each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int r = 0; r < 8; r += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + r], scale, -cs));
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + r + 1], scale, -cs));
+          l += p0 + p1;
+          hi[r >> 1] = pack2<E>(p0, p1);
+          if (PARTS == 2) lo[r >> 1] = pack2<E>(p0 - low<E>(hi[r >> 1]), p1 - high<E>(hi[r >> 1]));
+        }
+        ph[i] = __builtin_bit_cast(frag_t<E>, hi);
+        if (PARTS == 2) pl[i] = __builtin_bit_cast(frag_t<E>, lo);
+      }
+      const E* vb = vbuf + buf * TILE;
+      auto value = [&](int i, int d) {                 // V^T of 16 keys and 32 elements
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const E* p = vb + v_at[d & 3] + (d >> 2) * 128 + 16 * i * D;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+        const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * D));
+        const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_bit_cast(frag_t<E>, v);
+      };
+      uint32_t odd = 0u;                               // a value that is not finite, where some column does not see all
+      if (!full) {
+        for (int i = 0; i < TILE / 8; i += 64) {
+          const V16 x = ldv(vb + 8 * (i + lane));
+          const uint32_t e = __is_same(E, fp16) ? 0x7C007C00u : 0x7F807F80u, one = __is_same(E, fp16) ? 0x04000400u : 0x00800080u;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) odd |= ((x.w[w] & e) + one) & 0x80008000u;
+        }
+      }
+      if (__ballot(odd != 0u) == 0ull) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const frag_t<E> v = value(i, d);
+            acc[d] = mma32(v, ph[i], acc[d]);
+            if (PARTS == 2) acc[d] = mma32(v, pl[i], acc[d]);
+          }
+      } else {
+        // Such values count only for the columns that see their keys (0 times
+        // them would be NaN): key by key, the weights by way of LDS.
+        float* w = reinterpret_cast<float*>(lds + 4 * TILE * sizeof(E)) + wave * 16 * 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int x = left(i);
+          asm volatile("" : "+v"(x));                  // compared anew: 32 masks do not fit the registers
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float p = to_f(ph[i][r]) + (PARTS == 2 ? to_f(pl[i][r]) : 0.f);
+            w[(8 * (r >> 2) + 4 * f + (r & 3)) * 32 + n] = 8 * (r >> 2) + (r & 3) < x ? p : -1.f;
+          }
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) {
+            const float p = w[k * 32 + n];
+            const bool sees = !(p < 0.f);
+            const int key = 16 * i + k;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int r = 0; r < 16; r += 4) {
+                const f32x4 v = ld4f(vb + key * D + 8 * ((4 * d + (r >> 2)) ^ v_swap<D>(key)) + 4 * f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[d][r + j] = sees ? fmaf(p, v[j], acc[d][r + j]) : acc[d][r + j];
+                asm volatile("" ::: "memory");               // not all values at once
+              }
+          }
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+        }
+      }
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    int some = seen;
+    some |= __shfl_xor(some, 32, 64);
+    if (!real) continue;
+    if (part.whole) {
+      const float inv = some ? 1.f / l : 0.f;
+      const size_t rq = (size_t)row * a.Hq + head;
+      O* out = static_cast<O*>(a.o) + rq * D + 4 * f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          st4o(out + 32 * d + 2 * r, f32x4{acc[d][r] * inv, acc[d][r + 1] * inv, acc[d][r + 2] * inv, acc[d][r + 3] * inv});
+      if (f == 0 && a.lse != nullptr) a.lse[rq] = some ? (c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    } else {
+      const size_t at = ((size_t)(2 * slot + part.first) * heads + hm) * COLS + col;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          st4f(a.part_o + at * D + 4 * f + 32 * d + 2 * r, f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]});
+      if (f == 0) { a.part_ml[2 * at] = c; a.part_ml[2 * at + 1] = some ? l : -1.f; }
+    }
+  }
+}
+
+template <typename E, typename O, int D> hipError_t launch_d(const ChunkArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((chunk16_kernel<E, O, D, 2>), dim3((unsigned)(a.S * a.Hkv * a.MT)), dim3(64 * NW), 4 * KB * D * sizeof(E) + NW * 16 * 32 * sizeof(float), s, a);
+  return hipGetLastError();
+}
+
+template <typename E, typename O> hipError_t launch_o(const ChunkArgs& a, int d, hipStream_t s) {
+  if (d == 64) return launch_d<E, O, 64>(a, s);
+  if (d == 128) return launch_d<E, O, 128>(a, s);
+  return launch_d<E, O, 256>(a, s);
+}
+
+template <typename E> hipError_t launch_e(const ChunkArgs& a, int o_dtype, int d, hipStream_t s) {
+  if (o_dtype == 1) return launch_o<E, bf16>(a, d, s);
+  if (o_dtype == 2) return launch_o<E, fp16>(a, d, s);
+  return launch_o<E, float>(a, d, s);
+}
+
+}  // namespace
+
+hipError_t launch_chunk16(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {
+  return dtype == 1 ? launch_e<bf16>(a, o_dtype, d, s) : launch_e<fp16>(a, o_dtype, d, s);
+}
+
+}  // namespace sgdn

@@ -24,8 +24,12 @@ struct RopeArgs {
 };
 
 // A tile of the chunk attention: rows row0 .. row0 + rows - 1 of request req
-// (-1: of none).
-struct ChunkTile { int32_t row0, rows, req, pad; };
+// (-1: of none), which see up to `longest` tokens.  The tiles' costs (a unit for
+// each 64 keys and one more) stand in a row; `at` is where this one's begin.
+struct ChunkTile { int32_t row0, rows, req, longest; int64_t at; int64_t pad; };
+
+// What the plan finds: tiles, and the units of cost that a slot takes.
+struct ChunkHead { int64_t share; int32_t tiles; int32_t pad; };
 
 struct ChunkArgs {
   const void* q;
@@ -37,11 +41,15 @@ struct ChunkArgs {
   const int32_t* lens;
   void* o;
   float* lse;                // NULL: not wanted
-  int32_t* count;            // [1] tiles
+  ChunkHead* head;           // [1]
   ChunkTile* tiles;          // [cap]
+  int32_t* start;            // [S] the tile that a slot's first unit of cost lies in
+  float* part_o;             // [2 S][heads][columns][D] unnormalised outputs of parts of tiles
+  float* part_ml;            // [2 S][heads][columns][2] their softmax reference and sum (-1: nothing seen)
   int R, B, Hq, Hkv, G, lp, n_pages, W, max_len;
   int TR, GT, MT;            // rows of a tile, query heads of one, head tiles of a group
   int cap;                   // tiles at most
+  int S;                     // slots: workgroups of each head tile
   float scale;               // of the scores, times log2(e)
 };
 
@@ -49,8 +57,10 @@ struct ChunkArgs {
 int rope_slices(int R, int heads, int d, int dtype);
 hipError_t launch_rope(const RopeArgs& a, int dtype, int w_dtype, bool norm, bool interleaved, hipStream_t s);
 
-// Columns ((row, query head) pairs of one key/value head) of a tile.
-int chunk_columns(int dtype, int d);
+// Columns ((row, query head) pairs of one key/value head) of a tile, and the
+// workgroups that fill the chip.
+int chunk_columns(int dtype);
+int chunk_groups(int dtype, int d);
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 
 }  // namespace sgdn

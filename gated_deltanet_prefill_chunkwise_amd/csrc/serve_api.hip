@@ -67,20 +67,26 @@ int rope(const sgdn_rope_shape* p, const void* q, const void* k, bool norm, cons
              ? SGDN_OK : SGDN_EHIP;
 }
 
-struct ChunkPlan { int cap, TR, GT, MT; size_t off_tiles, total; };
+struct ChunkPlan { int cap, TR, GT, MT, S; size_t off_tiles, off_start, off_o, off_ml, total; };
 
-// False where a launch does not hold the tiles.
+// False where a launch does not hold the heads, or 32 bits the tiles.
 bool chunk_plan(const sgdn_paged* p, ChunkPlan* pl) {
-  const int cols = chunk_columns(p->dtype, p->d), G = p->n_q / p->n_kv;
+  const int cols = chunk_columns(p->dtype), G = p->n_q / p->n_kv;
   pl->GT = G < cols ? G : cols;
   pl->MT = (G + pl->GT - 1) / pl->GT;
   pl->TR = cols / pl->GT;
   // each request has one tile that is not full, and so have the rows of none (in front and behind)
   const int64_t cap = ((int64_t)p->rows + pl->TR - 1) / pl->TR + (p->batch < p->rows ? p->batch : p->rows) + 2;
-  if (too_many(cap * p->n_kv * pl->MT, 256)) return false;
+  const int64_t heads = (int64_t)p->n_kv * pl->MT, groups = chunk_groups(p->dtype, p->d);
+  if (too_many(heads, 256) || cap >= INT64_C(1) << 30) return false;
   pl->cap = (int)cap;
+  pl->S = (int)(groups > heads ? groups / heads : 1);
+  const size_t parts = 2 * (size_t)pl->S * heads * cols;
   pl->off_tiles = 256;
-  pl->total = pl->off_tiles + align256((size_t)cap * sizeof(ChunkTile));
+  pl->off_start = pl->off_tiles + align256((size_t)cap * sizeof(ChunkTile));
+  pl->off_o = pl->off_start + align256((size_t)pl->S * sizeof(int32_t));
+  pl->off_ml = pl->off_o + (pl->S > 1 ? align256(parts * p->d * sizeof(float)) : 0);
+  pl->total = pl->off_ml + (pl->S > 1 ? align256(parts * 2 * sizeof(float)) : 0);
   return true;
 }
 
@@ -155,11 +161,15 @@ int sgdn_paged_attend_chunk(const sgdn_paged* p, const void* q, int64_t ldq, con
   ChunkArgs a;
   a.q = q; a.ldq = ldq; a.kc = k_cache; a.vc = v_cache;
   a.table = table; a.cu = cu; a.lens = lens; a.o = o; a.lse = lse;
-  a.count = static_cast<int32_t*>(ws);
-  a.tiles = reinterpret_cast<ChunkTile*>(static_cast<char*>(ws) + pl.off_tiles);
+  char* w = static_cast<char*>(ws);
+  a.head = reinterpret_cast<ChunkHead*>(w);
+  a.tiles = reinterpret_cast<ChunkTile*>(w + pl.off_tiles);
+  a.start = reinterpret_cast<int32_t*>(w + pl.off_start);
+  a.part_o = reinterpret_cast<float*>(w + pl.off_o);
+  a.part_ml = reinterpret_cast<float*>(w + pl.off_ml);
   a.R = p->rows; a.B = p->batch; a.Hq = p->n_q; a.Hkv = p->n_kv; a.G = p->n_q / p->n_kv;
   a.lp = log2_page(p->page); a.n_pages = p->n_pages; a.W = p->width; a.max_len = longest(p);
-  a.TR = pl.TR; a.GT = pl.GT; a.MT = pl.MT; a.cap = pl.cap;
+  a.TR = pl.TR; a.GT = pl.GT; a.MT = pl.MT; a.cap = pl.cap; a.S = pl.S;
   a.scale = scale * 1.4426950408889634f;
   return launch_chunk(a, p->dtype, p->o_dtype, p->d, static_cast<hipStream_t>(stream)) == hipSuccess
              ? SGDN_OK : SGDN_EHIP;
