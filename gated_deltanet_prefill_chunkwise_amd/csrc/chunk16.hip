@@ -11,6 +11,8 @@
 //     in that order by two transposing reads.
 // So nothing crosses lanes between the products, and the running maximum, which
 // moves only where a score exceeds it by a threshold, is rarely shared.
+#include <type_traits>
+
 #include "chunk.h"
 
 namespace sgdn {
@@ -53,28 +55,38 @@ template <typename E> __device__ __forceinline__ float high(uint32_t w) {
 // 16-byte units of a row are permuted by the key's number, so that rows that are
 // read at once lie in different banks: unit u of key k is stored at u ^ f(k).
 // K is read 16 rows at once, one unit of each; V 4 or 8 rows, 64 or 32 bytes of each.
-template <int D> __device__ __forceinline__ int k_swap(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
-template <int D> __device__ __forceinline__ int v_swap(int key) {
+// f's bits are bits of k, so that f(k ^ k') = f(k) ^ f(k'): an address of another
+// unit or key is this one with some bits turned, and needs no register of its own.
+template <int D> __device__ __forceinline__ constexpr int k_swap(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
+template <int D> __device__ __forceinline__ constexpr int v_swap(int key) {
   return D == 64 ? ((key & 2) << 1) | ((key & 4) >> 1) : ((key & 3) << 2) | ((key & 4) >> 1);
 }
 
-// 16 bytes a lane from global memory to LDS (lane l to byte 16 l from `lds`).  In
-// asm, so that the compiler does not let every read of LDS wait for it: the
-// kernel waits itself, before the barrier in front of the block's first use.
-__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+// 16 bytes a lane from global memory to LDS (lane l to byte 16 l from `lds`), both
+// AT bytes on.  In asm, so that the compiler does not let every read of LDS wait
+// for it: the kernel waits itself, before the barrier in front of the block's
+// first use.
+template <int AT> __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" ::"s"(lds), "v"(offset), "s"(base), "n"(AT) : "memory", "m0");
+}
+// The J-th and later ones of 16 rows of keys (or values): 1 KiB each.
+template <int D, bool V, int J = 0> __device__ __forceinline__ void copy_rows(const char* base, uint32_t offset, uint32_t lds) {
+  constexpr int RPI = 512 / D;                       // rows of a copy
+  if constexpr (J * RPI < 16) {
+    copy_to_lds<(J & 3) * 1024>(base + (J >> 2) * 4096, offset ^ (16u * (V ? v_swap<D>(J * RPI) : k_swap<D>(J * RPI))), lds + (J >> 2) * 4096);
+    copy_rows<D, V, J + 1>(base, offset, lds);
+  }
 }
 
 template <typename E, typename O, int D, int PARTS>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(ChunkArgs a) {
   constexpr int NS = D / 16, DT = D / 32;            // reduction steps of the scores, 32-element tiles of an output
-  constexpr int U = D / 8, RPI = 64 / U, NI = 16 / RPI;   // units of a row, rows of a copy, copies of 16 keys
+  constexpr int U = D / 8;                           // 16-byte units of a row
   constexpr int TILE = KB * D;                       // elements of a block of keys
   constexpr float BIAS = __is_same(E, fp16) ? 10.f : 0.f;   // see paged_attend.hip
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-  E* const kbuf = reinterpret_cast<E*>(lds);         // two blocks of keys, then two of values
-  E* const vbuf = kbuf + 2 * TILE;
+  E* const vbuf = reinterpret_cast<E*>(lds) + 2 * TILE;   // two blocks of values, behind two of keys
 
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, f = lane >> 5;
@@ -85,22 +97,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
   const E* kc = static_cast<const E*>(a.kc);
   const E* vc = static_cast<const E*>(a.vc);
 
-  // byte offsets of this lane's part of the copies, from the first of 16 keys
-  uint32_t k_off[NI], v_off[NI];
-#pragma unroll
-  for (int j = 0; j < NI; ++j) {
-    const int key = j * RPI + lane / U, u = lane % U;
-    k_off[j] = (key * U + (u ^ k_swap<D>(key))) * 16;
-    v_off[j] = (key * U + (u ^ v_swap<D>(key))) * 16;
-  }
-  // elements at which this lane's reads of a block begin
-  int k_at[NS], v_at[DT < 4 ? DT : 4];
-#pragma unroll
-  for (int s = 0; s < NS; ++s) k_at[s] = n * D + 8 * ((2 * s + f) ^ k_swap<D>(n));
+  // bytes at which this lane's parts of the first copy begin, and its reads of a block
+  const uint32_t k_off = ((lane / U) * U + ((lane % U) ^ k_swap<D>(lane / U))) * 16;
+  const uint32_t v_off = ((lane / U) * U + ((lane % U) ^ v_swap<D>(lane / U))) * 16;
+  const int k_at = n * D * 2 + 16 * (f ^ k_swap<D>(n));
   const int m = lane & 15, v_key = 4 * f + (m >> 2);
-#pragma unroll
-  for (int d = 0; d < (DT < 4 ? DT : 4); ++d)
-    v_at[d] = v_key * D + 8 * ((4 * d + 2 * ((lane >> 4) & 1) + ((m & 3) >> 1)) ^ v_swap<D>(v_key)) + 4 * (m & 1);
+  const int v_at = v_key * D * 2 + 16 * ((2 * ((lane >> 4) & 1) + ((m & 3) >> 1)) ^ v_swap<D>(v_key)) + 8 * (m & 1);
 
   const int64_t share = a.head->share, begin = slot * share, end = begin + share;
   const int tiles = a.head->tiles;
@@ -124,6 +126,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
 #pragma unroll
       for (int s = 0; s < NS; ++s) qf[s] = ld8(q + 16 * s);
     }
+    // Here, once: a wait for them inside the loop would also wait for the copies there.
+    __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
     // A negative scale turns the query's sign, so that the largest product is the largest score.
     // A scale of 0 goes into the query whole, as 0 times a masked score is no score.
     if (a.scale <= 0.f) {
@@ -153,13 +157,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
       const int g = 4 * block + wave;
       const int page = max(__builtin_amdgcn_readlane(pages, g & 63), 0);      // a place that can be read
       const size_t from = ((size_t)page * a.Hkv + h) * P + (((int64_t)g << 4) & (P - 1));
-      const E* k = kc + from * D;
-      const E* v = vc + from * D;
       const uint32_t to = lds0 + (uint32_t)(buf * TILE + wave * 16 * D) * 2;
-#pragma unroll
-      for (int j = 0; j < NI; ++j) copy_to_lds(k, k_off[j], to + j * 1024);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) copy_to_lds(v, v_off[j], to + 2 * TILE * 2 + j * 1024);
+      copy_rows<D, false>(reinterpret_cast<const char*>(kc + from * D), k_off, to);
+      copy_rows<D, true>(reinterpret_cast<const char*>(vc + from * D), v_off, to + 2 * TILE * 2);
     };
 
     if (part.b0 < part.b1) {
@@ -167,11 +167,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
       lds_barrier();                                   // the last tile's blocks have been read
       copy(part.b0, 0);
     }
-    for (int b = part.b0; b < part.b1; ++b) {
+    // which of a block's 16 keys each lie in a page
+    auto valid_of = [&](int b) { return (uint32_t)(__ballot(pages >= 0) >> ((4 * b) & 63)) & 15u; };
+    // A block.  PLAIN: every column sees all of it.  (Copies of their own: the
+    // other case's rare branch costs the registers of the products 128 moves.)
+    auto step = [&](int b, uint32_t valid, auto PLAIN) {
       const int buf = (b - part.b0) & 1;
-      const uint64_t there = __ballot(pages >= 0);
-      const uint32_t valid = (uint32_t)(there >> ((4 * b) & 63)) & 15u;       // of this block's 16 keys each
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0)
       lds_barrier();                                   // this block is whole, the other buffer free
       if (b + 1 < part.b1) {
         if (((b + 1) & 15) == 0) look_up(b + 1);
@@ -179,26 +181,54 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
       }
       const int key0 = b * KB;
       // Places behind the last token and pages that are none may hold anything.
-      if (valid != 15u || key0 + KB > t.longest) {
+      if (!PLAIN && (valid != 15u || key0 + KB > t.longest)) {
         for (int i = tid; i < TILE / 8; i += 64 * NW) {
           const int key = i / U;
           if (!((valid >> (key >> 4)) & 1u) || key0 + key >= t.longest) stv(vbuf + buf * TILE + 8 * i, zv());
         }
         lds_barrier();
       }
-      if (!active || key0 >= len_hi) continue;
-      const bool full = valid == 15u && key0 + KB <= len_lo;
+      if (!active || (!PLAIN && key0 >= len_hi)) return;
+      const bool full = PLAIN || (valid == 15u && key0 + KB <= len_lo);
 
       f32x16 s[2];
       s[0] = zero16();
       s[1] = zero16();
-      const E* kb = kbuf + buf * TILE;
+      int k_from = k_at + buf * TILE * 2, v_from = v_at + (2 + buf) * TILE * 2;
+      asm volatile("" : "+v"(k_from), "+v"(v_from));   // formed anew for every block: their registers are few
+      constexpr int KS = NS < 4 ? NS : 4;              // steps whose keys are read at once
+      frag_t<E> kf[2][2 * KS];
+      auto keys = [&](int i0) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const frag_t<E> k0 = ld8(kb + k_at[i]), k1 = ld8(kb + k_at[i] + 32 * D);
-        s[0] = mma32(k0, qf[i], s[0]);
-        s[1] = mma32(k1, qf[i], s[1]);
+        for (int i = 0; i < KS; ++i) {
+          const E* k = reinterpret_cast<const E*>(lds + (k_from ^ (32 * (i0 + i))));
+          kf[(i0 / KS) & 1][2 * i] = ld8(k);
+          kf[(i0 / KS) & 1][2 * i + 1] = ld8(k + 32 * D);
+        }
+      };
+      keys(0);
+#pragma unroll
+      for (int i0 = 0; i0 < NS; i0 += KS) {
+        if (i0 + KS < NS) keys(i0 + KS);
+        __builtin_amdgcn_sched_barrier(0);             // the reads are requested in front of the products
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          s[0] = mma32(kf[(i0 / KS) & 1][2 * i], qf[i0 + i], s[0]);
+          s[1] = mma32(kf[(i0 / KS) & 1][2 * i + 1], qf[i0 + i], s[1]);
+        }
       }
+      auto value = [&](int i, int d) {                 // V^T of 16 keys and 32 elements
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const E* p = reinterpret_cast<const E*>(lds + (v_from ^ (64 * (d & 3)))) + (d >> 2) * 128 + 16 * i * D;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+        const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * D));
+        const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_bit_cast(frag_t<E>, v);
+      };
+      frag_t<E> vf[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vf[0][i] = value(i, 0);
+      __builtin_amdgcn_sched_barrier(0);
       // Of 16 keys number g this lane's column sees key 8 i + 4 f + j (i = 0, 1) where 8 i + j < left(g).
       auto left = [&](int g) { return (valid >> g) & 1u ? len - key0 - 16 * g - 4 * f : 0; };
       if (!full) {
@@ -229,30 +259,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
         for (int d = 0; d < DT; ++d) acc[d] *= g;
       }
       const float cs = c == -INFINITY ? 0.f : c;
-      frag_t<E> ph[4], pl[4];                          // of 16 keys each
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int r = 0; r < 8; r += 2) {
-          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + r], scale, -cs));
-          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + r + 1], scale, -cs));
-          l += p0 + p1;
-          hi[r >> 1] = pack2<E>(p0, p1);
-          if (PARTS == 2) lo[r >> 1] = pack2<E>(p0 - low<E>(hi[r >> 1]), p1 - high<E>(hi[r >> 1]));
-        }
-        ph[i] = __builtin_bit_cast(frag_t<E>, hi);
-        if (PARTS == 2) pl[i] = __builtin_bit_cast(frag_t<E>, lo);
-      }
       const E* vb = vbuf + buf * TILE;
-      auto value = [&](int i, int d) {                 // V^T of 16 keys and 32 elements
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const E* p = vb + v_at[d & 3] + (d >> 2) * 128 + 16 * i * D;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-        const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * D));
-        const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
-        return __builtin_bit_cast(frag_t<E>, v);
-      };
       uint32_t odd = 0u;                               // a value that is not finite, where some column does not see all
       if (!full) {
         for (int i = 0; i < TILE / 8; i += 64) {
@@ -262,16 +269,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
           for (int w = 0; w < 4; ++w) odd |= ((x.w[w] & e) + one) & 0x80008000u;
         }
       }
-      if (__ballot(odd != 0u) == 0ull) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const frag_t<E> v = value(i, d);
-            acc[d] = mma32(v, ph[i], acc[d]);
-            if (PARTS == 2) acc[d] = mma32(v, pl[i], acc[d]);
-          }
-      } else {
+      auto weight = [&](int i, int r) { return __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + r], scale, -cs)); };
+      if (!PLAIN && __ballot(odd != 0u) != 0ull) {
         // Such values count only for the columns that see their keys (0 times
         // them would be NaN): key by key, the weights by way of LDS.
         float* w = reinterpret_cast<float*>(lds + 4 * TILE * sizeof(E)) + wave * 16 * 32;
@@ -281,7 +280,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
           asm volatile("" : "+v"(x));                  // compared anew: 32 masks do not fit the registers
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const float p = to_f(ph[i][r]) + (PARTS == 2 ? to_f(pl[i][r]) : 0.f);
+            const float p = weight(i, r);
+            l += p;
             w[(8 * (r >> 2) + 4 * f + (r & 3)) * 32 + n] = 8 * (r >> 2) + (r & 3) < x ? p : -1.f;
           }
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -305,7 +305,41 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
           __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
           __builtin_amdgcn_wave_barrier();
         }
+        return;
       }
+      frag_t<E> ph[4], pl[4];                          // of 16 keys each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int r = 0; r < 8; r += 2) {
+          const float p0 = weight(i, r), p1 = weight(i, r + 1);
+          l += p0 + p1;
+          hi[r >> 1] = pack2<E>(p0, p1);
+          if (PARTS == 2) lo[r >> 1] = pack2<E>(p0 - low<E>(hi[r >> 1]), p1 - high<E>(hi[r >> 1]));
+        }
+        ph[i] = __builtin_bit_cast(frag_t<E>, hi);
+        if (PARTS == 2) pl[i] = __builtin_bit_cast(frag_t<E>, lo);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        if (d + 1 < DT) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vf[(d + 1) & 1][i] = value(i, d + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[d] = mma32(vf[d & 1][i], ph[i], acc[d]);
+          if (PARTS == 2) acc[d] = mma32(vf[d & 1][i], pl[i], acc[d]);
+        }
+      }
+    };
+    const int plain = min(part.b1, chunk_sees(a, t, t.row0) / KB);
+    for (int b = part.b0; b < part.b1; ++b) {
+      uint32_t valid = valid_of(b);
+      for (; b < plain && valid == 15u; valid = valid_of(++b)) step(b, valid, std::true_type{});
+      if (b < part.b1) step(b, valid, std::false_type{});
     }
 
     l += __shfl_xor(l, 32, 64);
