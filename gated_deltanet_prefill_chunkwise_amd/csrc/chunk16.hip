@@ -20,6 +20,7 @@ namespace sgdn {
 namespace {
 
 constexpr int KB = CHUNK_KEYS, COLS = CHUNK16_COLS, NW = 4;
+constexpr int GROUP = 6;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -43,13 +44,14 @@ template <typename E> __device__ __forceinline__ uint32_t pack2(float a, float b
   typedef E e2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, e2));
 }
-template <typename E> __device__ __forceinline__ float low(uint32_t w) {
-  if constexpr (__is_same(E, bf16)) return __builtin_bit_cast(float, w << 16);
-  else return to_f(__builtin_bit_cast(fp16, (uint16_t)w));
+// What the first of two numbers leaves of p, and the second.
+template <typename E> __device__ __forceinline__ float rest_low(float p, uint32_t w) {
+  if constexpr (__is_same(E, bf16)) return p - __builtin_bit_cast(float, w << 16);
+  else return p - to_f(__builtin_bit_cast(fp16, (uint16_t)w));
 }
-template <typename E> __device__ __forceinline__ float high(uint32_t w) {
-  if constexpr (__is_same(E, bf16)) return __builtin_bit_cast(float, w & 0xFFFF0000u);
-  else return to_f(__builtin_bit_cast(fp16, (uint16_t)(w >> 16)));
+template <typename E> __device__ __forceinline__ float rest_high(float p, uint32_t w) {
+  if constexpr (__is_same(E, bf16)) return p - __builtin_bit_cast(float, w & 0xFFFF0000u);
+  else return p - to_f(__builtin_bit_cast(fp16, (uint16_t)(w >> 16)));
 }
 
 // 16-byte units of a row are permuted by the key's number, so that rows that are
@@ -225,9 +227,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
         const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
         return __builtin_bit_cast(frag_t<E>, v);
       };
-      frag_t<E> vf[2][4];
+      frag_t<E> vf[2][DT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vf[0][i] = value(i, 0);
+      for (int d = 0; d < DT; ++d) vf[0][d] = value(0, d);
       __builtin_amdgcn_sched_barrier(0);
       // Of 16 keys number g this lane's column sees key 8 i + 4 f + j (i = 0, 1) where 8 i + j < left(g).
       auto left = [&](int g) { return (valid >> g) & 1u ? len - key0 - 16 * g - 4 * f : 0; };
@@ -307,31 +309,41 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
         }
         return;
       }
-      frag_t<E> ph[4], pl[4];                          // of 16 keys each
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      // The weights of 16 keys are formed while those of the 16 before are multiplied.
+      frag_t<E> ph[2], pl[2];
+      auto weights = [&](int i) {
         u32x4 hi, lo;
 #pragma unroll
         for (int r = 0; r < 8; r += 2) {
           const float p0 = weight(i, r), p1 = weight(i, r + 1);
           l += p0 + p1;
           hi[r >> 1] = pack2<E>(p0, p1);
-          if (PARTS == 2) lo[r >> 1] = pack2<E>(p0 - low<E>(hi[r >> 1]), p1 - high<E>(hi[r >> 1]));
+          if (PARTS == 2) lo[r >> 1] = pack2<E>(rest_low<E>(p0, hi[r >> 1]), rest_high<E>(p1, hi[r >> 1]));
         }
-        ph[i] = __builtin_bit_cast(frag_t<E>, hi);
-        if (PARTS == 2) pl[i] = __builtin_bit_cast(frag_t<E>, lo);
-      }
+        ph[i & 1] = __builtin_bit_cast(frag_t<E>, hi);
+        if (PARTS == 2) pl[i & 1] = __builtin_bit_cast(frag_t<E>, lo);
+      };
+      weights(0);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        if (d + 1 < DT) {
+      for (int i = 0; i < 4; ++i) {
+        if (i < 3) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vf[(d + 1) & 1][i] = value(i, d + 1);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int d = 0; d < DT; ++d) vf[(i + 1) & 1][d] = value(i + 1, d);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[d] = mma32(vf[d & 1][i], ph[i], acc[d]);
-          if (PARTS == 2) acc[d] = mma32(vf[d & 1][i], pl[i], acc[d]);
+        for (int d = 0; d < DT; ++d) acc[d] = mma32(vf[i & 1][d], ph[i & 1], acc[d]);
+        if (PARTS == 2) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) acc[d] = mma32(vf[i & 1][d], pl[i & 1], acc[d]);
+        }
+        if (i < 3) {
+          weights(i + 1);
+#pragma unroll
+          for (int m = 0; m < DT * PARTS; ++m) {       // a product, then as many others as hide behind it
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x402, GROUP, 0);
+          }
         }
       }
     };
