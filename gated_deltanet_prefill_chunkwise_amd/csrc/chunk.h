@@ -7,25 +7,23 @@
 namespace sgdn {
 
 constexpr int CHUNK_KEYS = 64;         // keys of a unit of cost
+constexpr int CHUNK_TILE = 4;          // units that a tile costs beside its keys
 constexpr int CHUNK16_COLS = 128;      // columns of a tile, 16-bit types
 
 __device__ __forceinline__ int chunk_blocks(int longest) { return (int)(((int64_t)longest + CHUNK_KEYS - 1) / CHUNK_KEYS); }
 
 // Tokens that row r sees.
 __device__ __forceinline__ int chunk_sees(const ChunkArgs& a, const ChunkTile& t, int r) {
-  if (t.req < 0) return 0;
-  const int64_t x = (int64_t)a.lens[t.req] - a.cu[t.req + 1] + r + 1;
-  return (int)min(max(x, (int64_t)0), (int64_t)a.max_len);
+  return (int)min(max(t.ahead + r + 1, (int64_t)0), (int64_t)a.max_len);
 }
 
 // The share of a slot (units of cost begin .. end - 1) of tile t: blocks b0 ..
-// b1 - 1.  Block j is unit t.at + 1 + j; the unit in front of the first is what a
-// tile costs beside its blocks.
+// b1 - 1.  Block j is unit t.at + CHUNK_TILE + j.
 struct ChunkPart { int b0, b1; bool whole, first; };
 
 __device__ __forceinline__ ChunkPart chunk_part(const ChunkTile& t, int64_t begin, int64_t end) {
   const int n = chunk_blocks(t.longest);
-  const int64_t lo = begin - t.at - 1, hi = end - t.at - 1;
+  const int64_t lo = begin - t.at - CHUNK_TILE, hi = end - t.at - CHUNK_TILE;
   ChunkPart p;
   p.b0 = (int)min(max(lo, (int64_t)0), (int64_t)n);
   p.b1 = (int)min(max(hi, (int64_t)0), (int64_t)n);

@@ -7,7 +7,7 @@
 //   p = 2^(x - c),  l += sum p,  A += V^T p;   c' > c: l, A *= 2^(c - c')
 //   o = A / l,  lse = (c + log2 l) ln 2
 //
-// Work: a tile costs a unit for each block of 64 keys and one more.  The costs of
+// Work: a tile costs a unit for each block of 64 keys and CHUNK_TILE more.  The costs of
 // all tiles, one after the other, are cut into S equal shares, a workgroup for
 // each share and head tile: whatever the lengths, all end together.  A tile
 // that a cut goes through is made in parts (at most two a workgroup that are not
@@ -18,7 +18,7 @@ namespace sgdn {
 
 namespace {
 
-constexpr int MIN_SHARE = 5;           // units of cost: a part of fewer blocks costs more to join than it saves
+constexpr int MIN_SHARE = CHUNK_TILE + 4;           // units of cost: a part of fewer blocks costs more to join than it saves
 
 // Tiles of every request, in order; then those of the rows that belong to none
 // (they write zeros).  One workgroup: the requests come in steps of 1024, a thread
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
   for (int64_t b0 = 0; b0 < (int64_t)a.B + 2; b0 += 1024) {
     const int64_t b = b0 + tid;
     int r0 = 0, r1 = 0;                // B: behind the last request, B + 1: in front of the first
-    int64_t ahead = -(INT64_C(1) << 40);   // row r sees ahead + r + 1 tokens
+    int64_t ahead = -(INT64_C(1) << 40);   // rows of none see none
     if (b < a.B) { r0 = a.cu[b]; r1 = a.cu[b + 1]; ahead = (int64_t)a.lens[b] - r1; }
     else if (b == a.B) { r0 = a.cu[a.B]; r1 = a.R; }
     else if (b == (int64_t)a.B + 1) { r1 = a.cu[0]; }
@@ -79,11 +79,12 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
           x.row0 = row0[lo] + (int)at;
           x.rows = min(a.TR, rows[lo] - (int)at);
           x.req = b0 + lo < a.B ? (int)(b0 + lo) : -1;
+          x.ahead = sees[lo];
           x.longest = (int)min(max(sees[lo] + x.row0 + x.rows, (int64_t)0), (int64_t)a.max_len);
         }
       }
       int64_t all;
-      x.at = cost + scan(mine ? (int64_t)chunk_blocks(x.longest) + 1 : (int64_t)0, sum_l, all);
+      x.at = cost + scan(mine ? (int64_t)chunk_blocks(x.longest) + CHUNK_TILE : (int64_t)0, sum_l, all);
       if (mine) a.tiles[base + t] = x;
       cost += all;
     }
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
   __syncthreads();
   // The slots that begin inside of a tile.
   for (int t = tid; t < base; t += 1024) {
-    const int64_t from = a.tiles[t].at, to = from + chunk_blocks(a.tiles[t].longest) + 1;
+    const int64_t from = a.tiles[t].at, to = from + chunk_blocks(a.tiles[t].longest) + CHUNK_TILE;
     for (int64_t s = (from + share - 1) / share; s * share < to; ++s) a.start[s] = t;
   }
 }
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
   const int tile = a.start[s + 1];
   if (tile >= a.head->tiles) return;
   const ChunkTile t = a.tiles[tile];
-  const int64_t share = a.head->share, to = t.at + chunk_blocks(t.longest) + 1;
+  const int64_t share = a.head->share, to = t.at + chunk_blocks(t.longest) + CHUNK_TILE;
   if (t.at >= (s + 1) * share || t.at / share != s) return;  // begins at the cut, or has one in front
   const int last = (int)((to - 1) / share);
   const int h = hm / a.MT, mt = hm - h * a.MT, gt = min(a.GT, a.G - mt * a.GT);

@@ -108,26 +108,30 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
 
   const int64_t share = a.head->share, begin = slot * share, end = begin + share;
   const int tiles = a.head->tiles;
-  for (int ti = a.start[slot]; ti < tiles; ++ti) {
-    const ChunkTile t = a.tiles[ti];
+  int ti = a.start[slot];
+  ChunkTile next;
+  if (ti < tiles) next = a.tiles[ti];
+  while (ti < tiles) {
+    const ChunkTile t = next;
     if (t.at >= end) break;
+    if (++ti < tiles) next = a.tiles[ti];              // here, so that it is there when it is wanted
     if (t.rows <= 0) continue;
     const ChunkPart part = chunk_part(t, begin, end);
-    const int col = 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
-    const bool real = my_row < t.rows && my_head < gt;
-    const int row = t.row0 + min(my_row, t.rows - 1), head = head0 + min(my_head, gt - 1);
-    // columns that are none see what their row does: they change nothing
-    const int len = chunk_sees(a, t, row);
+    int len;                                           // that this lane's column sees
+    const E* q;
+    {                                                  // columns that are none see what their row does: they change nothing
+      const int col = 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
+      const int row = t.row0 + min(my_row, t.rows - 1), head = head0 + min(my_head, gt - 1);
+      len = chunk_sees(a, t, row);
+      q = static_cast<const E*>(a.q) + row * a.ldq + (size_t)head * D + 8 * f;
+    }
     const int len_lo = __builtin_amdgcn_readlane(len, 0), len_hi = __builtin_amdgcn_readlane(len, 31);
     const bool active = 32 * wave < t.rows * a.GT;
     const int32_t* table = a.table + (size_t)max(t.req, 0) * a.W;
 
     frag_t<E> qf[NS];
-    {
-      const E* q = static_cast<const E*>(a.q) + row * a.ldq + (size_t)head * D + 8 * f;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) qf[s] = ld8(q + 16 * s);
-    }
+    for (int s = 0; s < NS; ++s) qf[s] = ld8(q + 16 * s);
     // Here, once: a wait for them inside the loop would also wait for the copies there.
     __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
     // A negative scale turns the query's sign, so that the largest product is the largest score.
@@ -174,6 +178,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
     // A block.  PLAIN: every column sees all of it.  (Copies of their own: the
     // other case's rare branch costs the registers of the products 128 moves.)
     auto step = [&](int b, uint32_t valid, auto PLAIN) {
+      // What the rare case needs is formed there: kept from block to block it
+      // would cost registers (and, spilled, waits for the copies).
+      int lane = lane_id();
+      if (!PLAIN) asm volatile("" : "+v"(lane));
+      const int n = lane & 31, f = lane >> 5;
       const int buf = (b - part.b0) & 1;
       __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0)
       lds_barrier();                                   // this block is whole, the other buffer free
@@ -357,7 +366,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
     l += __shfl_xor(l, 32, 64);
     int some = seen;
     some |= __shfl_xor(some, 32, 64);
-    if (!real) continue;
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));                     // as in the rare case above
+    const int n = lane & 31, f = lane >> 5;
+    const int col = 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
+    if (my_row >= t.rows || my_head >= gt) continue;
+    const int row = t.row0 + my_row, head = head0 + my_head;
     if (part.whole) {
       const float inv = some ? 1.f / l : 0.f;
       const size_t rq = (size_t)row * a.Hq + head;
@@ -381,7 +395,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
 }
 
 template <typename E, typename O, int D> hipError_t launch_d(const ChunkArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((chunk16_kernel<E, O, D, 2>), dim3((unsigned)(a.S * a.Hkv * a.MT)), dim3(64 * NW), 4 * KB * D * sizeof(E) + NW * 16 * 32 * sizeof(float), s, a);
+  hipLaunchKernelGGL((chunk16_kernel<E, O, D, __is_same(O, float) ? 2 : 1>), dim3((unsigned)(a.S * a.Hkv * a.MT)), dim3(64 * NW), 4 * KB * D * sizeof(E) + NW * 16 * 32 * sizeof(float), s, a);
   return hipGetLastError();
 }
 

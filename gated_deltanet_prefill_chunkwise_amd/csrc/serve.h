@@ -24,9 +24,10 @@ struct RopeArgs {
 };
 
 // A tile of the chunk attention: rows row0 .. row0 + rows - 1 of request req
-// (-1: of none), which see up to `longest` tokens.  The tiles' costs (a unit for
-// each 64 keys and one more) stand in a row; `at` is where this one's begin.
-struct ChunkTile { int32_t row0, rows, req, longest; int64_t at; int64_t pad; };
+// (-1: of none).  Row r sees ahead + r + 1 tokens, the last row `longest`.  The
+// tiles' costs (CHUNK_TILE units and one for each 64 keys) stand in a row; `at` is
+// where this one's begin.
+struct ChunkTile { int32_t row0, rows, req, longest; int64_t at, ahead; };
 
 // What the plan finds: tiles, and the units of cost that a slot takes.
 struct ChunkHead { int64_t share; int32_t tiles; int32_t pad; };

@@ -1,6 +1,7 @@
 """GPU parity of the attention of chunks against the fp64 oracle: the bounds are those of the
-attention of single rows (test_gpu_paged.check), with weights of 16-bit inputs in two parts
-whatever the output's type, as the header says: 2^-17 (bf16) and 2^-23 (fp16) of sum p |v|."""
+attention of single rows (test_gpu_paged.check).  Weights of 16-bit inputs err by 2^-17 (bf16) or
+2^-23 (fp16) of themselves for an fp32 output, where they enter in two parts, and by half a step
+of the type (2^-8, 2^-11) for a 16-bit one, as the header says; by nothing with fp32 inputs."""
 import numpy as np
 import pytest
 
@@ -25,7 +26,8 @@ def check(o, lse, want, out, dtype, D):
     small = 2.0 ** -35 * s["n"] if dtype == "f16" else 0.0
     vmax = s.get("vmax", np.zeros(rl.shape))
     tiny = 2.0 ** -25 if out == "f16" else 1e-30          # half the smallest step of an fp16 o
-    tol = s["absv"] * (TWO_PARTS[dtype] + 2 * score + 2 * sums)[..., None] + U[out] * np.abs(ro) + tiny + (small * vmax)[..., None] * np.ones(D)
+    weight = TWO_PARTS[dtype] if out == "f32" or dtype == "f32" else U[dtype]
+    tol = s["absv"] * (weight + 2 * score + 2 * sums)[..., None] + U[out] * np.abs(ro) + tiny + (small * vmax)[..., None] * np.ones(D)
     err = np.abs(o - ro)
     worst = float((err / tol).max())
     ltol = (score + sums + 4 * u * np.abs(np.where(empty, 0, rl)) + 2.0 ** -22)[~empty]
