@@ -217,7 +217,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
           kf[(i0 / KS) & 1][2 * i + 1] = ld8(k + 32 * D);
         }
       };
-      keys(0);
+      __builtin_amdgcn_s_setprio(0); keys(0);
 #pragma unroll
       for (int i0 = 0; i0 < NS; i0 += KS) {
         if (i0 + KS < NS) keys(i0 + KS);
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
       } else {
         seen = true;
       }
-      float mx = s[0][0];
+      __builtin_amdgcn_s_setprio(1); float mx = s[0][0];
 #pragma unroll
       for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
 #pragma unroll
