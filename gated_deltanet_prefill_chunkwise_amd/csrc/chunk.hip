@@ -103,13 +103,15 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
   }
 }
 
-// Parts of a tile: (column, element) of the parts by slots s0, s0 + 1, .. in
-// that order.  A workgroup takes a cut between slots s and s + 1, if it is the
-// first of its tile, a head tile and 16 of its columns.
-template <typename O, int D, int COLS>
+// Joins the parts of a tile, of slots s, s + 1, ..: a workgroup takes the cut
+// between slots s and s + 1, if it is the first of its tile, a head tile and the
+// CW columns of a wave.  Parts lie as in that wave's registers, 4 elements a lane:
+// run i of 64 lanes holds, of column n = lane % CW, elements e(i, lane) .. + 3.
+template <typename O, int D, int COLS, int CW>
 __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
-  const int heads = a.Hkv * a.MT, slices = COLS / 16;
-  const int slice = blockIdx.x % slices, hm = blockIdx.x / slices % heads, s = blockIdx.x / slices / heads;
+  constexpr int NR = CW * D / 256;                           // runs of a wave's columns
+  const int heads = a.Hkv * a.MT, waves = COLS / CW;
+  const int wave = blockIdx.x % waves, hm = blockIdx.x / waves % heads, s = blockIdx.x / waves / heads;
   const int tile = a.start[s + 1];
   if (tile >= a.head->tiles) return;
   const ChunkTile t = a.tiles[tile];
@@ -117,37 +119,37 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
   if (t.at >= (s + 1) * share || t.at / share != s) return;  // begins at the cut, or has one in front
   const int last = (int)((to - 1) / share);
   const int h = hm / a.MT, mt = hm - h * a.MT, gt = min(a.GT, a.G - mt * a.GT);
-  constexpr int EL = 16 * D / 256;                           // elements of a thread
-  const int col = 16 * slice + threadIdx.x / 16, e0 = (threadIdx.x % 16) * 4;
-  const int my_row = col / a.GT, my_head = col - my_row * a.GT;
+  const int lane = lane_id(), i0 = threadIdx.x >> 6;
+  const int col = wave * CW + lane % CW, my_row = col / a.GT, my_head = col - my_row * a.GT;
   if (my_row >= t.rows || my_head >= gt) return;
+  auto part = [&](int i) { return ((size_t)(i == s ? 2 * s + 1 : 2 * i) * heads + hm) * COLS; };
   float m = -INFINITY;
-  auto at = [&](int i) { return ((size_t)(i == s ? 2 * s + 1 : 2 * i) * heads + hm) * COLS + col; };
-  for (int i = s; i <= last; ++i) m = fmaxf(m, a.part_ml[2 * at(i)]);
+  for (int i = s; i <= last; ++i) m = fmaxf(m, a.part_ml[2 * (part(i) + col)]);
   float sum = 0.f;
   bool any = false;
-  f32x4 acc[EL / 4];
+  f32x4 acc[NR / 4];
 #pragma unroll
-  for (int e = 0; e < EL / 4; ++e) acc[e] = zero4();
+  for (int k = 0; k < NR / 4; ++k) acc[k] = zero4();
   for (int i = s; i <= last; ++i) {
-    const size_t p = at(i);
-    const float c = a.part_ml[2 * p], l = a.part_ml[2 * p + 1];
+    const float c = a.part_ml[2 * (part(i) + col)], l = a.part_ml[2 * (part(i) + col) + 1];
     if (l == -1.f) continue;                                 // saw nothing
     any = true;
     if (c == -INFINITY) { if (!(l <= 0.f)) sum += l; continue; }   // scores of -inf alone, or NaN
     const float w = __builtin_amdgcn_exp2f(c - m);
     sum += l * w;
+    const float* from = a.part_o + (part(i) + wave * CW) * D + 4 * lane;
 #pragma unroll
-    for (int e = 0; e < EL / 4; ++e) acc[e] += w * *reinterpret_cast<const f32x4*>(a.part_o + p * D + e0 + 64 * e);
+    for (int k = 0; k < NR / 4; ++k) acc[k] += w * *reinterpret_cast<const f32x4*>(from + (i0 + 4 * k) * 256);
   }
   const size_t rq = (size_t)(t.row0 + my_row) * a.Hq + h * a.G + mt * a.GT + my_head;
 #pragma unroll
-  for (int e = 0; e < EL / 4; ++e) {
-    f32x4 o = acc[e];
+  for (int k = 0; k < NR / 4; ++k) {
+    const int i = i0 + 4 * k, e = CW == 32 ? 32 * (i >> 2) + 8 * (i & 3) + 4 * (lane >> 5) : 16 * i + 4 * (lane >> 4);
+    f32x4 o = acc[k];
     if (any) o /= sum;
-    st4o(static_cast<O*>(a.o) + rq * D + e0 + 64 * e, o);
+    st4o(static_cast<O*>(a.o) + rq * D + e, o);
   }
-  if (e0 == 0 && a.lse != nullptr) a.lse[rq] = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (i0 == 0 && lane < CW && a.lse != nullptr) a.lse[rq] = any ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // fp32: 64 columns a tile, 16 a wave; keys and values in stages of 32 through
@@ -288,10 +290,10 @@ __global__ __launch_bounds__(256) void chunk32_kernel(ChunkArgs a) {
       for (int d = 0; d < DT; ++d) st4o(out + 16 * d, some ? acc[d] / l : zero4());
       if (g == 0 && a.lse != nullptr) a.lse[rq] = some ? (c + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else {
-      const size_t at = ((size_t)(2 * slot + part.first) * heads + hm) * COLS32 + col;
+      const size_t at = ((size_t)(2 * slot + part.first) * heads + hm) * COLS32 + 16 * wave;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) st4f(a.part_o + at * D + 16 * d + 4 * g, acc[d]);
-      if (g == 0) { a.part_ml[2 * at] = c; a.part_ml[2 * at + 1] = some ? l : -1.f; }
+      for (int d = 0; d < DT; ++d) st4f(a.part_o + at * D + d * 256 + 4 * lane, acc[d]);
+      if (g == 0) { a.part_ml[2 * (at + n)] = c; a.part_ml[2 * (at + n) + 1] = some ? l : -1.f; }
     }
   }
 }
@@ -306,8 +308,8 @@ template <typename O, int D> hipError_t launch_d(const ChunkArgs& a, int dtype, 
   hipError_t e = dtype == 0 ? launch32<O, D>(a, s) : launch_chunk16(a, dtype, o_dtype, D, s);
   if (e != hipSuccess || a.S == 1) return e;
   const int cuts = (a.S - 1) * a.Hkv * a.MT;
-  if (dtype == 0) hipLaunchKernelGGL((join_kernel<O, D, COLS32>), dim3(cuts * (COLS32 / 16)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((join_kernel<O, D, CHUNK16_COLS>), dim3(cuts * (CHUNK16_COLS / 16)), dim3(256), 0, s, a);
+  if (dtype == 0) hipLaunchKernelGGL((join_kernel<O, D, COLS32, 16>), dim3(cuts * (COLS32 / 16)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((join_kernel<O, D, CHUNK16_COLS, 32>), dim3(cuts * (CHUNK16_COLS / 32)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

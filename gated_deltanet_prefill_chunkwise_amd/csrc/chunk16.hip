@@ -369,27 +369,47 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
     int lane = lane_id();
     asm volatile("" : "+v"(lane));                     // as in the rare case above
     const int n = lane & 31, f = lane >> 5;
-    const int col = 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
-    if (my_row >= t.rows || my_head >= gt) continue;
-    const int row = t.row0 + my_row, head = head0 + my_head;
     if (part.whole) {
+      // By way of LDS, so that a wave writes whole rows: 16-byte unit u of column k at u ^ k.
+      constexpr int OU = D * (int)sizeof(O) / 16, SWAP = OU < 16 ? OU - 1 : 15;
+      char* mine = lds + wave * 32 * D * (int)sizeof(O);
       const float inv = some ? 1.f / l : 0.f;
-      const size_t rq = (size_t)row * a.Hq + head;
-      O* out = static_cast<O*>(a.o) + rq * D + 4 * f;
+      lds_barrier();                                   // all waves are done with the last block
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          st4o(out + 32 * d + 2 * r, f32x4{acc[d][r] * inv, acc[d][r + 1] * inv, acc[d][r + 2] * inv, acc[d][r + 3] * inv});
-      if (f == 0 && a.lse != nullptr) a.lse[rq] = some ? (c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        for (int r = 0; r < 16; r += 4) {
+          const int at = (32 * d + 2 * r + 4 * f) * (int)sizeof(O);
+          st4o(reinterpret_cast<O*>(mine + n * D * (int)sizeof(O) + ((at >> 4) ^ (n & SWAP)) * 16 + (at & 15)),
+               f32x4{acc[d][r] * inv, acc[d][r + 1] * inv, acc[d][r + 2] * inv, acc[d][r + 3] * inv});
+        }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      auto place = [&](int k) {                        // of the wave's column k among the call's rows and heads, -1 for none
+        const int col = 32 * wave + k, my_row = col / a.GT, my_head = col - my_row * a.GT;
+        return my_row < t.rows && my_head < gt ? (int64_t)(t.row0 + my_row) * a.Hq + head0 + my_head : (int64_t)-1;
+      };
+      for (int i = lane; i < 32 * OU; i += 64) {
+        const int k = i / OU, u = i % OU;
+        const int64_t rq = place(k);
+        if (rq >= 0) stv(static_cast<char*>(a.o) + (rq * OU + u) * 16, ldv(mine + (k * OU + (u ^ (k & SWAP))) * 16));
+      }
+      if (f == 0 && a.lse != nullptr) {
+        const int64_t rq = place(n);
+        if (rq >= 0) a.lse[rq] = some ? (c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
     } else {
-      const size_t at = ((size_t)(2 * slot + part.first) * heads + hm) * COLS + col;
+      // Parts as they lie in the registers: the join reads them so.
+      const size_t at = ((size_t)(2 * slot + part.first) * heads + hm) * COLS + 32 * wave;
+      if (active) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          st4f(a.part_o + at * D + 4 * f + 32 * d + 2 * r, f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]});
-      if (f == 0) { a.part_ml[2 * at] = c; a.part_ml[2 * at + 1] = some ? l : -1.f; }
+          for (int r = 0; r < 16; r += 4)
+            st4f(a.part_o + at * D + (4 * d + (r >> 2)) * 256 + 4 * lane, f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]});
+        if (f == 0) { a.part_ml[2 * (at + n)] = c; a.part_ml[2 * (at + n) + 1] = some ? l : -1.f; }
+      }
     }
   }
 }
