@@ -7,7 +7,7 @@
 //   p = 2^(x - c),  l += sum p,  A += V^T p;   c' > c: l, A *= 2^(c - c')
 //   o = A / l,  lse = (c + log2 l) ln 2
 //
-// Work: each block of 64 keys has a cost, and so has a tile (chunk.h).  The costs of
+// Work: a tile costs a unit for each block of 64 keys and CHUNK_TILE more.  The costs of
 // all tiles, one after the other, are cut into S equal shares, a workgroup for
 // each share and head tile: whatever the lengths, all end together.  A tile
 // that a cut goes through is made in parts (at most two a workgroup that are not
@@ -18,7 +18,7 @@ namespace sgdn {
 
 namespace {
 
-constexpr int MIN_SHARE = CHUNK_TILE + 4 * CHUNK_COST;           // units of cost: a part of fewer blocks costs more to join than it saves
+constexpr int MIN_SHARE = CHUNK_TILE + 4;           // units of cost: a part of fewer blocks costs more to join than it saves
 
 // Tiles of every request, in order; then those of the rows that belong to none
 // (they write zeros).  One workgroup: the requests come in steps of 1024, a thread
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
         }
       }
       int64_t all;
-      x.at = cost + scan(mine ? chunk_cost_all(a, x) : (int64_t)0, sum_l, all);
+      x.at = cost + scan(mine ? (int64_t)chunk_blocks(x.longest) + CHUNK_TILE : (int64_t)0, sum_l, all);
       if (mine) a.tiles[base + t] = x;
       cost += all;
     }
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
   __syncthreads();
   // The slots that begin inside of a tile.
   for (int t = tid; t < base; t += 1024) {
-    const int64_t from = a.tiles[t].at, to = from + chunk_cost_all(a, a.tiles[t]);
+    const int64_t from = a.tiles[t].at, to = from + chunk_blocks(a.tiles[t].longest) + CHUNK_TILE;
     for (int64_t s = (from + share - 1) / share; s * share < to; ++s) a.start[s] = t;
   }
 }
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
   const int tile = a.start[s + 1];
   if (tile >= a.head->tiles) return;
   const ChunkTile t = a.tiles[tile];
-  const int64_t share = a.head->share, to = t.at + chunk_cost_all(a, t);
+  const int64_t share = a.head->share, to = t.at + chunk_blocks(t.longest) + CHUNK_TILE;
   if (t.at >= (s + 1) * share || t.at / share != s) return;  // begins at the cut, or has one in front
   const int last = (int)((to - 1) / share);
   const int h = hm / a.MT, mt = hm - h * a.MT, gt = min(a.GT, a.G - mt * a.GT);
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256) void chunk32_kernel(ChunkArgs a) {
     const ChunkTile t = a.tiles[ti];
     if (t.at >= end) break;
     if (t.rows <= 0) continue;
-    const ChunkPart part = chunk_part(a, t, begin, end);
+    const ChunkPart part = chunk_part(t, begin, end);
     const int col = 16 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
     const bool real = my_row < t.rows && my_head < gt;
     const int row = t.row0 + min(my_row, t.rows - 1), head = head0 + min(my_head, gt - 1);
@@ -325,8 +325,6 @@ int chunk_columns(int dtype) { return dtype == 0 ? COLS32 : CHUNK16_COLS; }
 
 // Two workgroups a CU, one where its LDS holds no more.
 int chunk_groups(int, int d) { return d == 256 ? 256 : 512; }
-
-int chunk_single_cost(int dtype, int heads) { return dtype == 0 || heads > 32 ? CHUNK_COST : CHUNK_COST_SINGLE; }
 
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {
   if (o_dtype == 1) return launch_o<bf16>(a, dtype, o_dtype, d, s);

@@ -116,13 +116,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
     if (t.at >= end) break;
     if (++ti < tiles) next = a.tiles[ti];              // here, so that it is there when it is wanted
     if (t.rows <= 0) continue;
-    const ChunkPart part = chunk_part(a, t, begin, end);
-    // A single row: the waves divide its keys, not its columns.
-    const bool narrow = t.rows == 1 && gt <= 32;
+    const ChunkPart part = chunk_part(t, begin, end);
     int len;                                           // that this lane's column sees
     const E* q;
     {                                                  // columns that are none see what their row does: they change nothing
-      const int col = narrow ? n : 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
+      const int col = 32 * wave + n, my_row = col / a.GT, my_head = col - my_row * a.GT;
       const int row = t.row0 + min(my_row, t.rows - 1), head = head0 + min(my_head, gt - 1);
       len = chunk_sees(a, t, row);
       q = static_cast<const E*>(a.q) + row * a.ldq + (size_t)head * D + 8 * f;
@@ -173,7 +171,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
     if (part.b0 < part.b1) {
       look_up(part.b0 & ~15);
       lds_barrier();                                   // the last tile's blocks have been read
-      if (!narrow) copy(part.b0, 0);
+      copy(part.b0, 0);
     }
     // which of a block's 16 keys each lie in a page
     auto valid_of = [&](int b) { return (uint32_t)(__ballot(pages >= 0) >> ((4 * b) & 63)) & 15u; };
@@ -358,166 +356,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
         }
       }
     };
-    // A single row's part of keys: each wave takes 32 keys of every 128, has its
-    // own place in LDS for them and waits for nobody; the next keys are requested
-    // when these have been read, and so are the values.  All columns see the same
-    // keys, so that none needs a second look.
-    auto single_row = [&] {
-      constexpr int HALF = 32 * D, COPIES = HALF * 2 / 1024;
-      int lane = lane_id();
-      asm volatile("" : "+v"(lane));                   // as in step()
-      const int f = lane >> 5, m = lane & 15, v_key = 4 * f + (m >> 2), j1 = 2 * part.b1;
-      const int k_from = wave * 2 * HALF * 2 + (lane & 31) * D * 2 + 16 * (f ^ k_swap<D>(lane & 31));
-      const int v_from = (wave * 2 + 1) * HALF * 2 + v_key * D * 2 + 16 * ((2 * ((lane >> 4) & 1) + ((m & 3) >> 1)) ^ v_swap<D>(v_key)) + 8 * (m & 1);
-      auto copy_half = [&](int j, auto V) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int g = 2 * j + i;
-          const int page = max(__builtin_amdgcn_readlane(pages, g & 63), 0);    // a place that can be read
-          const size_t from = (((size_t)page * a.Hkv + h) * P + (((int64_t)g << 4) & (P - 1))) * D;
-          copy_rows<D, V>(reinterpret_cast<const char*>((V ? vc : kc) + from), V ? v_off : k_off,
-                          lds0 + (uint32_t)((wave * 2 + V) * HALF + i * 16 * D) * 2);
-        }
-      };
-      auto there = [&](int j) { return (uint32_t)(__ballot(pages >= 0) >> ((2 * j) & 63)) & 3u; };
-      int j = 2 * part.b0 + wave;
-      uint32_t valid = 0;
-      if (j < j1) {
-        if ((j >> 5) != (part.b0 >> 4)) look_up((j >> 5) << 4);
-        copy_half(j, std::false_type{});
-        copy_half(j, std::true_type{});
-        valid = there(j);
-      }
-      while (j < j1) {
-        const int next = j + 4, key0 = 32 * j;
-        const bool more = next < j1;
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(COPIES) : "memory");           // the keys, not the values behind them
-        f32x16 s = zero16();
-        {
-          frag_t<E> kf[NS];
-#pragma unroll
-          for (int i = 0; i < NS; ++i) kf[i] = ld8(reinterpret_cast<const E*>(lds + (k_from ^ (32 * i))));
-          __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0): they have been read
-          __builtin_amdgcn_sched_barrier(0);
-          const uint32_t now = valid;
-          if (more) {
-            if ((next >> 5) != (j >> 5)) look_up((next >> 5) << 4);
-            copy_half(next, std::false_type{});
-            valid = there(next);
-          }
-#pragma unroll
-          for (int i = 0; i < NS; ++i) s = mma32(kf[i], qf[i], s);
-          if (now != 3u || key0 + 32 > len) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int key = 8 * (r >> 2) + 4 * f + (r & 3);
-              if (key0 + key >= len || !((now >> (r >> 3)) & 1u)) s[r] = -INFINITY;
-            }
-          }
-          seen = seen || now != 0u;                    // key0 < len: the part ends with the row's last block
-          float mx = s[0];
-#pragma unroll
-          for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
-          mx *= scale;
-          if (__ballot(mx > c + (BIAS + 4.f)) != 0ull) {
-            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-            const float cn = fmaxf(c, mx - BIAS);
-            const float g = cn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(c - cn);
-            c = cn;
-            l *= g;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) acc[d] *= g;
-          }
-          const float cs = c == -INFINITY ? 0.f : c;
-          u32x4 ph[2], pl[2];
-#pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[r], scale, -cs)), p1 = __builtin_amdgcn_exp2f(fmaf(s[r + 1], scale, -cs));
-            l += p0 + p1;
-            const uint32_t w = pack2<E>(p0, p1);
-            ph[r >> 3][(r & 7) >> 1] = w;
-            if (PARTS == 2) pl[r >> 3][(r & 7) >> 1] = pack2<E>(rest_low<E>(p0, w), rest_high<E>(p1, w));
-          }
-          if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(COPIES) : "memory");   // the values, not the keys behind them
-          else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            u32x4 keep;                                // of this lane's eight keys: what is behind the last may be no number
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int key = key0 + 16 * i + 8 * (w >> 1) + 4 * f + 2 * (w & 1);
-              const bool in = (now >> i) & 1u;
-              keep[w] = (in && key < len ? 0xFFFFu : 0u) | (in && key + 1 < len ? 0xFFFF0000u : 0u);
-            }
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              typedef short s16x8 __attribute__((ext_vector_type(8)));
-              const E* p = reinterpret_cast<const E*>(lds + (v_from ^ (64 * (d & 3)))) + (d >> 2) * 128 + 16 * i * D;
-              const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-              const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * D));
-              const s16x8 v = __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7);
-              const frag_t<E> vf = __builtin_bit_cast(frag_t<E>, __builtin_bit_cast(u32x4, v) & keep);
-              acc[d] = mma32(vf, __builtin_bit_cast(frag_t<E>, ph[i]), acc[d]);
-              if (PARTS == 2) acc[d] = mma32(vf, __builtin_bit_cast(frag_t<E>, pl[i]), acc[d]);
-            }
-          }
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0): they have been read
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) copy_half(next, std::true_type{});
-        j = next;
-      }
-      // Join the waves: all to the largest reference, then wave 0 adds them up.
-      float* ml = reinterpret_cast<float*>(lds + 4 * TILE * sizeof(E));          // [wave][2][64]
-      ml[wave * 128 + lane] = c;
-      ml[wave * 128 + 64 + lane] = seen ? 1.f : 0.f;
-      lds_barrier();                                   // also: all keys and values have been read
-      float top = -INFINITY;
-      bool any = false;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        top = fmaxf(top, fmaxf(ml[w * 128 + lane], ml[w * 128 + (lane ^ 32)]));
-        any = any || ml[w * 128 + 64 + lane] != 0.f;
-      }
-      const float mine = c == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(c - top);
-      float* out = reinterpret_cast<float*>(lds) + wave * 32 * D + 4 * lane;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          st4f(out + (4 * d + (r >> 2)) * 256, f32x4{acc[d][r] * mine, acc[d][r + 1] * mine, acc[d][r + 2] * mine, acc[d][r + 3] * mine});
-      // A wave whose scores are all -inf has a sum of 0, or NaN where one of them is.
-      const float lw = c == -INFINITY ? (l <= 0.f ? 0.f : l) : l * mine;
-      lds_barrier();
-      ml[wave * 128 + lane] = lw;
-      lds_barrier();
-      if (wave == 0) {
-        l = 0.f;
-        for (int w = 0; w < NW; ++w) l += ml[w * 128 + lane];
-        c = top;
-        seen = any;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            f32x4 x = zero4();
-#pragma unroll
-            for (int w = 0; w < NW; ++w) x += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds) + w * 32 * D + 4 * lane + (4 * d + (r >> 2)) * 256);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[d][r + e] = x[e];
-          }
-      }
-    };
-
-    if (narrow) {
-      if (part.b0 < part.b1) single_row();
-    } else {
-      const int plain = min(part.b1, chunk_sees(a, t, t.row0) / KB);
-      for (int b = part.b0; b < part.b1; ++b) {
-        uint32_t valid = valid_of(b);
-        for (; b < plain && valid == 15u; valid = valid_of(++b)) step(b, valid, std::true_type{});
-        if (b < part.b1) step(b, valid, std::false_type{});
-      }
+    const int plain = min(part.b1, chunk_sees(a, t, t.row0) / KB);
+    for (int b = part.b0; b < part.b1; ++b) {
+      uint32_t valid = valid_of(b);
+      for (; b < plain && valid == 15u; valid = valid_of(++b)) step(b, valid, std::true_type{});
+      if (b < part.b1) step(b, valid, std::false_type{});
     }
 
     l += __shfl_xor(l, 32, 64);

@@ -25,7 +25,8 @@ struct RopeArgs {
 
 // A tile of the chunk attention: rows row0 .. row0 + rows - 1 of request req
 // (-1: of none).  Row r sees ahead + r + 1 tokens, the last row `longest`.  The
-// tiles' costs stand in a row; `at` is where this one's begin.
+// tiles' costs (CHUNK_TILE units and one for each 64 keys) stand in a row; `at` is
+// where this one's begin.
 struct ChunkTile { int32_t row0, rows, req, longest; int64_t at, ahead; };
 
 // What the plan finds: tiles, and the units of cost that a slot takes.
@@ -50,7 +51,6 @@ struct ChunkArgs {
   int TR, GT, MT;            // rows of a tile, query heads of one, head tiles of a group
   int cap;                   // tiles at most
   int S;                     // slots: workgroups of each head tile
-  int single;                // cost of a block of a single row
   float scale;               // of the scores, times log2(e)
 };
 
@@ -62,7 +62,6 @@ hipError_t launch_rope(const RopeArgs& a, int dtype, int w_dtype, bool norm, boo
 // workgroups that fill the chip.
 int chunk_columns(int dtype);
 int chunk_groups(int dtype, int d);
-int chunk_single_cost(int dtype, int heads);   // of a tile
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 
 }  // namespace sgdn
