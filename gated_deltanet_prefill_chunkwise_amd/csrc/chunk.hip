@@ -18,16 +18,18 @@ namespace sgdn {
 
 namespace {
 
-constexpr int MIN_SHARE = CHUNK_TILE + 4;           // units of cost: a part of fewer blocks costs more to join than it saves
+constexpr int MIN_SHARE = 4;           // units of cost: a part of fewer blocks costs more to join than it saves
 
 // Tiles of every request, in order; then those of the rows that belong to none
-// (they write zeros).  One workgroup: the requests come in steps of 1024, a thread
+// (they write zeros).  One workgroup: the requests come in steps of NT, a thread
 // each, and so do each step's tiles, which find their request in the sums of
-// tiles by bisection.
-__global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
-  __shared__ int first[1025], row0[1024], rows[1024], sum_i[16];
-  __shared__ int64_t sees[1024], sum_l[16];
-  __shared__ int64_t total_cost;
+// tiles by bisection.  Latency: 256 threads, where they hold all requests and
+// tiles, sooner agree on a sum.
+template <int NT>
+__global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
+  constexpr int NW = NT / 64;
+  __shared__ int first[NT], row0[NT], rows[NT], sum_i[NW];
+  __shared__ int64_t sees[NT], sum_l[NW];
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
   // exclusive sums over the workgroup
   auto scan = [&](auto x, auto* part, auto& total) {
@@ -37,17 +39,17 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
       const auto y = __shfl_up(s, o, 64);
       if (lane >= o) s += y;
     }
-    __syncthreads();
     if (lane == 63) part[wave] = s;
     __syncthreads();
     auto before = s - x;
     total = 0;
-    for (int w = 0; w < 16; ++w) { if (w < wave) before += part[w]; total += part[w]; }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) { if (w < wave) before += part[w]; total += part[w]; }
     return before;
   };
-  int base = 0;
-  int64_t cost = 0;
-  for (int64_t b0 = 0; b0 < (int64_t)a.B + 2; b0 += 1024) {
+  int base = 0, mine = -1;             // this thread's tile of the last step
+  int64_t cost = 0, from = 0, to = 0;  // ... and what it takes
+  for (int64_t b0 = 0; b0 < (int64_t)a.B + 2; b0 += NT) {
     const int64_t b = b0 + tid;
     int r0 = 0, r1 = 0;                // B: behind the last request, B + 1: in front of the first
     int64_t ahead = -(INT64_C(1) << 40);   // rows of none see none
@@ -64,17 +66,17 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
     sees[tid] = ahead;
     first[tid] = before;
     __syncthreads();
-    for (int t0 = 0; t0 < total; t0 += 1024) {
-      const int t = t0 + tid;
-      const bool mine = t < total && (int64_t)base + t < a.cap;
+    for (int64_t t0 = 0; t0 < total; t0 += NT) {
+      const int64_t t = t0 + tid;
       ChunkTile x{0, 0, -1, 0, 0, 0};  // stays so where cu falls and the sums mean nothing
-      if (mine) {
-        int lo = 0, hi = 1023;         // the last request whose first tile is t or one in front
+      mine = t < total && base + t < a.cap ? (int)(base + t) : -1;
+      if (mine >= 0) {
+        int lo = 0, hi = NT - 1;       // the last request whose first tile is t or one in front
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
           if (first[mid] <= t) lo = mid; else hi = mid - 1;
         }
-        const int64_t at = ((int64_t)t - first[lo]) * a.TR;
+        const int64_t at = (t - first[lo]) * a.TR;
         if (at >= 0 && at < rows[lo]) {
           x.row0 = row0[lo] + (int)at;
           x.rows = min(a.TR, rows[lo] - (int)at);
@@ -84,22 +86,32 @@ __global__ __launch_bounds__(1024) void plan_kernel(ChunkArgs a) {
         }
       }
       int64_t all;
-      x.at = cost + scan(mine ? (int64_t)chunk_blocks(x.longest) + CHUNK_TILE : (int64_t)0, sum_l, all);
-      if (mine) a.tiles[base + t] = x;
+      const int64_t takes = mine >= 0 ? (int64_t)chunk_blocks(x.longest) + CHUNK_TILE : 0;
+      x.at = cost + scan(takes, sum_l, all);
+      if (mine >= 0) a.tiles[mine] = x;
+      from = x.at;
+      to = x.at + takes;
       cost += all;
+      __syncthreads();                 // before the next sums
     }
     base = (int)min((int64_t)base + total, (int64_t)a.cap);
     __syncthreads();
   }
   const int64_t share = max((cost + a.S - 1) / a.S, (int64_t)MIN_SHARE);
-  if (tid == 0) { *a.head = ChunkHead{share, base, 0}; total_cost = cost; }
-  for (int s = tid; s < a.S; s += 1024)
+  if (tid == 0) *a.head = ChunkHead{share, base, 0};
+  for (int s = tid; s < a.S; s += NT)
     if (s * share >= cost) a.start[s] = base;               // nothing to do
-  __syncthreads();
   // The slots that begin inside of a tile.
-  for (int t = tid; t < base; t += 1024) {
-    const int64_t from = a.tiles[t].at, to = from + chunk_blocks(a.tiles[t].longest) + CHUNK_TILE;
+  auto begins = [&](int t, int64_t from, int64_t to) {
     for (int64_t s = (from + share - 1) / share; s * share < to; ++s) a.start[s] = t;
+  };
+  if (base <= NT && (int64_t)a.B + 2 <= NT) {               // a step of requests and one of tiles: they are at hand
+    if (mine >= 0) begins(mine, from, to);
+    return;
+  }
+  for (int t = tid; t < base; t += NT) {
+    const int64_t at = a.tiles[t].at;
+    begins(t, at, at + chunk_blocks(a.tiles[t].longest) + CHUNK_TILE);
   }
 }
 
@@ -123,23 +135,37 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
   const int col = wave * CW + lane % CW, my_row = col / a.GT, my_head = col - my_row * a.GT;
   if (my_row >= t.rows || my_head >= gt) return;
   auto part = [&](int i) { return ((size_t)(i == s ? 2 * s + 1 : 2 * i) * heads + hm) * COLS; };
-  float m = -INFINITY;
-  for (int i = s; i <= last; ++i) m = fmaxf(m, a.part_ml[2 * (part(i) + col)]);
-  float sum = 0.f;
+  // A running reference, as the keys have: one pass, the next parts on their way.
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  float m = -INFINITY, sum = 0.f;
   bool any = false;
   f32x4 acc[NR / 4];
 #pragma unroll
   for (int k = 0; k < NR / 4; ++k) acc[k] = zero4();
-  for (int i = s; i <= last; ++i) {
-    const float c = a.part_ml[2 * (part(i) + col)], l = a.part_ml[2 * (part(i) + col) + 1];
-    if (l == -1.f) continue;                                 // saw nothing
-    any = true;
-    if (c == -INFINITY) { if (!(l <= 0.f)) sum += l; continue; }   // scores of -inf alone, or NaN
-    const float w = __builtin_amdgcn_exp2f(c - m);
-    sum += l * w;
-    const float* from = a.part_o + (part(i) + wave * CW) * D + 4 * lane;
+  constexpr int AT_ONCE = NR > 16 ? 2 : 4;
+  for (int i = s; i <= last; i += AT_ONCE) {
+    float2 x[AT_ONCE];
+    f32x4 o[AT_ONCE][NR / 4];
 #pragma unroll
-    for (int k = 0; k < NR / 4; ++k) acc[k] += w * *reinterpret_cast<const f32x4*>(from + (i0 + 4 * k) * 256);
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const size_t p = part(min(i + j, last));
+      x[j] = ml[p + col];
+      const float* from = a.part_o + (p + wave * CW) * D + 4 * lane;
+#pragma unroll
+      for (int k = 0; k < NR / 4; ++k) o[j][k] = *reinterpret_cast<const f32x4*>(from + (i0 + 4 * k) * 256);
+    }
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const float c = x[j].x, l = x[j].y;
+      if (i + j > last || l == -1.f) continue;               // saw nothing
+      any = true;
+      if (c == -INFINITY) { if (!(l <= 0.f)) sum += l; continue; }   // scores of -inf alone, or NaN
+      const float top = fmaxf(m, c), w = __builtin_amdgcn_exp2f(c - top), f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      sum = fmaf(l, w, sum * f);
+#pragma unroll
+      for (int k = 0; k < NR / 4; ++k) acc[k] = acc[k] * f + w * o[j][k];
+    }
   }
   const size_t rq = (size_t)(t.row0 + my_row) * a.Hq + h * a.G + mt * a.GT + my_head;
 #pragma unroll
@@ -304,7 +330,8 @@ template <typename O, int D> hipError_t launch32(const ChunkArgs& a, hipStream_t
 }
 
 template <typename O, int D> hipError_t launch_d(const ChunkArgs& a, int dtype, int o_dtype, hipStream_t s) {
-  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, s, a);
+  if (a.B + 2 <= 256 && a.cap <= 256) hipLaunchKernelGGL(plan_kernel<256>, dim3(1), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(plan_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
   hipError_t e = dtype == 0 ? launch32<O, D>(a, s) : launch_chunk16(a, dtype, o_dtype, D, s);
   if (e != hipSuccess || a.S == 1) return e;
   const int cuts = (a.S - 1) * a.Hkv * a.MT;
