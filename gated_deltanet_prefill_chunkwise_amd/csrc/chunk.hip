@@ -222,27 +222,49 @@ __global__ __launch_bounds__(256) void chunk32_kernel(ChunkArgs a) {
     for (int d = 0; d < DT; ++d) acc[d] = zero4();
 
     const int k1 = (int)min((int64_t)part.b1 * CHUNK_KEYS, (int64_t)t.longest);
-    for (int k0 = part.b0 * CHUNK_KEYS; k0 < k1; k0 += SK) {
-      // Halves of 16 keys: page of each, none beyond the table.
-      int page[2];
+    // Pages of the halves of 16 keys, none beyond the table.
+    struct Pages { int p[2]; };
+    auto pages = [&](int k0) {
+      Pages x;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int64_t j = ((int64_t)k0 + 16 * hf) >> a.lp;
-        const int x = j < a.W ? table[j] : -1;
-        page[hf] = x >= 0 && x < a.n_pages ? x : -1;
+        const int p = j < a.W ? table[j] : -1;
+        x.p[hf] = p >= 0 && p < a.n_pages ? p : -1;
+      }
+      return x;
+    };
+    // A stage goes through registers: the next one is on its way while this one is used.
+    constexpr int NU = 2 * SK * RU / 256;                  // 16-byte units of a thread
+    V16 units[NU];
+    auto fetch = [&](int k0, const Pages& pg) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int i = tid + 256 * u, key = i % (SK * RU) / RU, p = key < 16 ? pg.p[0] : pg.p[1];
+        units[u] = zv();
+        if (p >= 0 && k0 + key < t.longest)
+          units[u] = ldv((u >= NU / 2 ? vc : kc) + (((size_t)p * a.Hkv + h) * P + ((k0 + key) & (P - 1))) * D + (i % RU) * 4);
+      }
+    };
+    const int all_see = chunk_sees(a, t, t.row0);          // keys that every column sees
+    Pages next{{-1, -1}};
+    if (part.b0 < part.b1) {
+      next = pages(part.b0 * CHUNK_KEYS);
+      fetch(part.b0 * CHUNK_KEYS, next);
+    }
+    for (int k0 = part.b0 * CHUNK_KEYS; k0 < k1; k0 += SK) {
+      const int page[2] = {next.p[0], next.p[1]};
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int i = tid + 256 * u, key = i % (SK * RU) / RU;
+        stv((u >= NU / 2 ? vs : ks) + key * LD + (i % RU) * 4, units[u]);
       }
       __syncthreads();
-      for (int i = tid; i < 2 * SK * RU; i += 256) {
-        const bool is_v = i >= SK * RU;
-        const int key = i % (SK * RU) / RU, u = i % RU, pg = key < 16 ? page[0] : page[1];
-        V16 x = zv();
-        if (pg >= 0 && k0 + key < t.longest) {
-          const size_t from = (((size_t)pg * a.Hkv + h) * P + ((k0 + key) & (P - 1))) * D + u * 4;
-          x = ldv((is_v ? vc : kc) + from);
-        }
-        stv((is_v ? vs : ks) + key * LD + u * 4, x);
+      if (k0 + SK < k1) {
+        next = pages(k0 + SK);
+        fetch(k0 + SK, next);
       }
-      __syncthreads();
       f32x4 s0 = zero4(), s1 = zero4();
       const int key = 8 * (n >> 2) + (n & 3);              // of K's row n in the first product; 4 more in the second
 #pragma unroll
@@ -280,8 +302,10 @@ __global__ __launch_bounds__(256) void chunk32_kernel(ChunkArgs a) {
       }
       // A value that is not finite counts only for columns that see its key: key by key there.
       bool odd = false;
-      for (int i = tid; i < SK * D; i += 256) odd = odd || !__builtin_isfinite(vs[(i / D) * LD + i % D]);
-      if (__syncthreads_or(odd)) {
+      if (k0 + SK > all_see) {
+        for (int i = lane; i < SK * D; i += 64) odd |= !__builtin_isfinite(vs[(i / D) * LD + i % D]);
+      }
+      if (__ballot(odd) != 0ull) {
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
