@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
 constexpr int SK = 32, COLS32 = 64;
 
 template <typename O, int D>
-__global__ __launch_bounds__(256) void chunk32_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(256, D == 64 ? 4 : 2) void chunk32_kernel(ChunkArgs a) {
   constexpr int NS = D / 32, DT = D / 16, LD = D + 4, RU = D / 4;
   __shared__ __attribute__((aligned(16))) float ks[SK * LD];
   __shared__ __attribute__((aligned(16))) float vs[SK * LD];
@@ -374,8 +374,9 @@ template <typename O> hipError_t launch_o(const ChunkArgs& a, int dtype, int o_d
 
 int chunk_columns(int dtype) { return dtype == 0 ? COLS32 : CHUNK16_COLS; }
 
-// Two workgroups a CU, one where its LDS holds no more.
-int chunk_groups(int, int d) { return d == 256 ? 256 : 512; }
+// Two workgroups a CU, one where its LDS holds no more (16 bits, D = 256), four
+// where registers and LDS hold them (fp32, D = 64: chunk of 301 rows 71 us, 80 with two).
+int chunk_groups(int dtype, int d) { return dtype == 0 ? (d == 64 ? 1024 : 512) : d == 256 ? 256 : 512; }
 
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {
   if (o_dtype == 1) return launch_o<bf16>(a, dtype, o_dtype, d, s);
