@@ -55,7 +55,7 @@ struct ChunkArgs {
 };
 
 // dtype: the boundary's sgdn_dtype values (0 fp32, 1 bf16, 2 fp16)
-int rope_slices(int R, int heads, int d, int dtype);
+int rope_slices(int R, int Hq, int Hk, int d, int dtype);
 hipError_t launch_rope(const RopeArgs& a, int dtype, int w_dtype, bool norm, bool interleaved, hipStream_t s);
 
 // Columns ((row, query head) pairs of one key/value head) of a tile, and the

@@ -62,7 +62,7 @@ int rope(const sgdn_rope_shape* p, const void* q, const void* k, bool norm, cons
   a.R = p->rows; a.Hq = p->n_q; a.Hk = p->n_k; a.D = p->d; a.rot = p->rot;
   a.pos = pos; a.pos_offset = pos_offset; a.freqs = freqs; a.magnitude = (float)magnitude;
   a.wq = wq; a.wk = wk; a.w_offset = w_offset; a.eps = eps;
-  a.slices = rope_slices(p->rows, p->n_q + p->n_k, p->d, p->dtype);
+  a.slices = rope_slices(p->rows, p->n_q, p->n_k, p->d, p->dtype);
   return launch_rope(a, p->dtype, p->w_dtype, norm, p->layout == SGDN_ROPE_INTERLEAVED, static_cast<hipStream_t>(stream)) == hipSuccess
              ? SGDN_OK : SGDN_EHIP;
 }
