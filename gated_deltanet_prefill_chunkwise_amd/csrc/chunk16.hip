@@ -11,6 +11,28 @@
 //     in that order by two transposing reads.
 // So nothing crosses lanes between the products, and the running maximum, which
 // moves only where a score exceeds it by a threshold, is rarely shared.
+//
+// Weights enter the second product rounded to the type: for a 16-bit output in
+// one part, an error of half a step of the type like the output's own rounding;
+// for an fp32 output in two, the second what the rounding of the first left.
+// (A prompt of 8192 tokens below: 618 us in one part, 770 in two, for half as
+// many products again.)  All else is fp32.
+//
+// Bound: the matrix cores' power.  32 / 8 heads of 128, bf16, page 64:
+//   a prompt of 8192 tokens    546 us, 1007 TFLOP/s (a library product of
+//                              8192^3: 1273); the clock falls to 1.9 GHz
+//   4 x up to 1024 tokens over 16384 cached and 60 single rows over as many
+//                              1080 us; 2.7 GB and 694 GFLOP would each take 545
+//   127 single rows over up to 8192 tokens   510 us, what reading the cache takes
+// and 16 / 2 heads of 256, 512 tokens over 131072: 1262 us, 871 TFLOP/s.
+// Of 3290 clocks a block 129 are waits for the copies; no LDS bank conflicts.
+// Tried (the prompt; boxes differ by 7 %): 8 waves and 256 columns 578 us against
+// 569, though the step of prompts and rows then reads 4.4 GB of HBM and not 7.3;
+// those 8 in halves half a block apart 1057 against 906 (prompts and rows); the
+// scores of the next 64 keys between the weights of these 710 against 618, of the
+// next 32 790 against 624 (registers).  A raised priority of waves that form
+// weights: 589 -> 581 us, prompts and rows 1150 -> 1115.  Waves that divide the
+// keys of single rows among them: 526 against 510 us (127 rows).
 #include <type_traits>
 
 #include "chunk.h"
@@ -20,7 +42,7 @@ namespace sgdn {
 namespace {
 
 constexpr int KB = CHUNK_KEYS, COLS = CHUNK16_COLS, NW = 4;
-constexpr int GROUP = 6;
+constexpr int GROUP = 6;               // instructions behind a product (6, 8, 10: 785, 790, 793 us, two parts)
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -217,7 +239,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
           kf[(i0 / KS) & 1][2 * i + 1] = ld8(k + 32 * D);
         }
       };
-      __builtin_amdgcn_s_setprio(0); keys(0);
+      __builtin_amdgcn_s_setprio(0);
+      keys(0);
 #pragma unroll
       for (int i0 = 0; i0 < NS; i0 += KS) {
         if (i0 + KS < NS) keys(i0 + KS);
@@ -254,7 +277,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
       } else {
         seen = true;
       }
-      __builtin_amdgcn_s_setprio(1); float mx = s[0][0];
+      __builtin_amdgcn_s_setprio(1);                   // a wave that forms weights goes first: products of others hide behind it
+      float mx = s[0][0];
 #pragma unroll
       for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
 #pragma unroll

@@ -51,6 +51,11 @@ int rope(const sgdn_rope_shape* p, const void* q, const void* k, bool norm, cons
   if (bad_heads(q, p->q, p->n_q, p) || bad_heads(k, p->k, p->n_k, p) || bad_heads(q_out, p->q_out, p->n_q, p) ||
       bad_heads(k_out, p->k_out, p->n_k, p))
     return SGDN_EINVAL;
+  // in place: the same rows and heads
+  auto moved = [p](const void* in, const void* out, int n, const sgdn_strides& i, const sgdn_strides& o) {
+    return n > 0 && in == out && ((p->rows > 1 && i.row != o.row) || (n > 1 && i.head != o.head));
+  };
+  if (moved(q, q_out, p->n_q, p->q, p->q_out) || moved(k, k_out, p->n_k, p->k, p->k_out)) return SGDN_EINVAL;
   RopeArgs a;
   // strides of a single row or head: no distance, and no overflow either
   auto side = [p](const void* in, void* out, int n, const sgdn_strides& i, const sgdn_strides& o) {
@@ -69,16 +74,17 @@ int rope(const sgdn_rope_shape* p, const void* q, const void* k, bool norm, cons
 
 struct ChunkPlan { int cap, TR, GT, MT, S; size_t off_tiles, off_start, off_o, off_ml, total; };
 
-// False where a launch does not hold the heads, or 32 bits the tiles.
+// False where a launch does not hold the heads.
 bool chunk_plan(const sgdn_paged* p, ChunkPlan* pl) {
   const int cols = chunk_columns(p->dtype), G = p->n_q / p->n_kv;
   pl->GT = G < cols ? G : cols;
   pl->MT = (G + pl->GT - 1) / pl->GT;
   pl->TR = cols / pl->GT;
-  // each request has one tile that is not full, and so have the rows of none (in front and behind)
+  // each request has one tile that is not full, and so have the rows of none (in
+  // front and behind); rows < 2^26, so that 32 bits hold them
   const int64_t cap = ((int64_t)p->rows + pl->TR - 1) / pl->TR + (p->batch < p->rows ? p->batch : p->rows) + 2;
   const int64_t heads = (int64_t)p->n_kv * pl->MT, groups = chunk_groups(p->dtype, p->d);
-  if (too_many(heads, 256) || cap >= INT64_C(1) << 30) return false;
+  if (too_many(heads, 256)) return false;
   pl->cap = (int)cap;
   pl->S = (int)(groups > heads ? groups / heads : 1);
   const size_t parts = 2 * (size_t)pl->S * heads * cols;

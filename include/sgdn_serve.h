@@ -94,7 +94,7 @@ typedef struct {
  * p = pos[r] + pos_offset:  magnitude (x cos t - y sin t, y cos t + x sin t).
  *   q, k         [rows, heads, d] inputs (NULL without heads); q_out, k_out
  *                outputs: either the inputs themselves (the same data and
- *                strides) or without any overlap
+ *                strides; SGDN_EINVAL for other strides) or without any overlap
  *   pos          [rows]; a row with p < 0 is left out: nothing of it is read or
  *                written.  (pos = row_len of sgdn_paged_plan, pos_offset = -1:
  *                each new token's place, and nothing for padding rows.)
@@ -124,14 +124,17 @@ int sgdn_norm_rope(const sgdn_rope_shape* p, const void* q, const void* k, const
 
 /* ---- Attention of chunks over the paged cache ------------------------- */
 
-/* Device workspace of sgdn_paged_attend_chunk; 0 for an invalid shape. */
+/* Device workspace of sgdn_paged_attend_chunk; 0 for an invalid shape.  Up to
+ * 68 MB for parts of work (34 MB for heads of 64) and 32 bytes for each request
+ * and each tile of rows (128 (row, query head of one key head) pairs, 64 in
+ * fp32).  What it holds does not matter. */
 size_t sgdn_paged_chunk_workspace_bytes(const sgdn_paged* p);
 
 /* sgdn_paged_attend for steps in which requests have many new tokens (prompts,
  * pieces of prompts, drafts), or some of them many and others one: a request's
  * context is read once for many rows, and the work is divided on the device by
- * the lengths it finds there.  For steps of single rows alone sgdn_paged_attend
- * is as fast or faster.
+ * the lengths it finds there.  (Single rows alone take as long here as there,
+ * a few of them longer: its three launches take 17 us at least.)
  *   cu           [B + 1] rows of request b are cu[b] .. cu[b + 1] - 1 (cu of
  *                sgdn_paged_plan; must not fall)
  *   lens         [B] tokens of each request, its new ones included (lens_out of
@@ -140,10 +143,17 @@ size_t sgdn_paged_chunk_workspace_bytes(const sgdn_paged* p);
  *                positive, at most max_len).
  * All else as in sgdn_paged_attend: q, table, scale, o, lse, rows that see
  * nothing (rows of no request among them: o = 0, lse = -inf), pages that are
- * none, types, precision, supported shapes.  A row's bits may depend on the
- * other rows of its request and on the lengths of the call's requests, by which
- * the sums are divided; its error bound does not.
- * rows + batch < 2^30 / n_kv (SGDN_EUNSUPPORTED otherwise). */
+ * none, types, supported shapes.  Where cu falls, which request a row belongs
+ * to is undefined, and rows may be left unwritten.
+ * Precision: as sgdn_paged_attend, but with 16-bit inputs the softmax weights
+ * enter their product rounded to the type where o is 16-bit too (an error of at
+ * most 2^-8 in bf16, 2^-11 in fp16, of the weighted mean of |v|), and in two
+ * parts where it is fp32 (2^-17; 2^-23 and 2^-35 of the largest weight for each
+ * key).  A row's bits may depend on the other rows of its request and on the
+ * lengths of the call's requests, by which the sums are divided; its error
+ * bound does not.  Equal calls give equal bits.
+ * n_kv ceil(n_q / n_kv / 128) < 2^24 - 7 (64 for 128 in fp32); SGDN_EUNSUPPORTED
+ * otherwise. */
 int sgdn_paged_attend_chunk(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache,
                             const void* v_cache, const int32_t* table, const int32_t* cu,
                             const int32_t* lens, float scale, void* o, float* lse, void* ws,

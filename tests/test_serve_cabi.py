@@ -130,6 +130,7 @@ ROPE_REFUSED = [
     (dict(q_row=1016), EINVAL),                       # rows that overlap
     (dict(ko_row=0), EINVAL), (dict(ko_head=0), EINVAL), (dict(qo_row=-1024), EINVAL), (dict(q_row=(1 << 36) + 8), EINVAL),
     (dict(q_head=128, q_row=128), EINVAL),            # heads of a row on the next row's
+    (dict(qo_row=2048), EINVAL), (dict(ko_row=512, ko_head=256), EINVAL),   # in place, with other strides
 ]
 
 
@@ -175,7 +176,7 @@ CHUNK_REFUSED = [
     (dict(rows=-1), EINVAL), (dict(n_q=0), EINVAL), (dict(n_kv=0), EINVAL), (dict(d=0), EINVAL), (dict(page=0), EINVAL),
     (dict(n_pages=0), EINVAL), (dict(dtype=3), EINVAL), (dict(o_dtype=3), EINVAL), (dict(d=96), EUNSUPPORTED),
     (dict(page=48), EUNSUPPORTED), (dict(n_q=9), EUNSUPPORTED), (dict(n_pages=1 << 26), EUNSUPPORTED),
-    (dict(rows=1 << 26), EUNSUPPORTED), (dict(batch=0), EINVAL), (dict(width=0), EINVAL), (dict(max_len=-1), EINVAL),
+    (dict(rows=1 << 26), EUNSUPPORTED), (dict(n_q=(1 << 24) - 7, n_kv=(1 << 24) - 7), EUNSUPPORTED), (dict(batch=0), EINVAL), (dict(width=0), EINVAL), (dict(max_len=-1), EINVAL),
     (dict(max_len=20 * 64 + 1), EINVAL), (dict(width=1 << 26), EUNSUPPORTED),
     (dict(scale=float("nan")), EINVAL), (dict(scale=3e38), EINVAL), (dict(ldq=1020), EINVAL), (dict(ldq=1028), EINVAL),
 ]
