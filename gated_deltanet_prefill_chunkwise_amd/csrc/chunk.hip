@@ -11,12 +11,14 @@
 // all tiles, one after the other, are cut into S equal shares, a workgroup for
 // each share and head tile: whatever the lengths, all end together.  A tile
 // that a cut goes through is made in parts (at most two a workgroup that are not
-// whole tiles), which the join adds up by the rule above.
+// whole tiles), which the join adds up by the rule above.  Shares are larger than
+// that where the longest tile would fall into more parts than are worth joining.
 //
 // Measured (plan, attention, join): 16 rows over 4096 tokens, 32 / 8 heads of 128,
-// bf16: 5.2, 11 and 9 us; fp32, 3 prompts of up to 301 rows over up to 1501 tokens,
-// 15 / 3 heads of 64: 5.1, 65 and 7 us.  The plan is latency (a chain of sums), the join
-// reads the parts once, four at a time (one by one: 13.4 us).
+// bf16: 5.2, 11 and 7 us; fp32, 3 prompts of up to 301 rows over up to 1501 tokens,
+// 15 / 3 heads of 64: 6, 65 and 7 us.  The plan is latency (a chain of sums), the join
+// reads the parts once, four at a time (one by one: 13.4 us for the 16 rows) and by
+// four sets of waves (one set: 9.2).
 #include "chunk.h"
 
 namespace sgdn {
@@ -35,7 +37,7 @@ constexpr int MIN_SHARE = 4;
 template <int NT>
 __global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
   constexpr int NW = NT / 64;
-  __shared__ int row0[NT], rows[NT];
+  __shared__ int row0[NT], rows[NT], most;
   __shared__ int64_t first[NT], sees[NT], part[NW];
   const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6;
   // exclusive sums over the workgroup
@@ -54,6 +56,7 @@ __global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
     for (int w = 0; w < NW; ++w) { if (w < wave) before += part[w]; total += part[w]; }
     return before;
   };
+  if (tid == 0) most = 0;              // blocks of the longest tile
   int base = 0, mine = -1;             // this thread's tile of the last step
   int64_t cost = 0, from = 0, to = 0;  // ... and what it takes
   for (int64_t b0 = 0; b0 < (int64_t)a.B + 2; b0 += NT) {
@@ -94,7 +97,10 @@ __global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
       int64_t all;
       const int64_t takes = mine >= 0 ? (int64_t)chunk_blocks(x.longest) + CHUNK_TILE : 0;
       x.at = cost + scan(takes, all);
-      if (mine >= 0) a.tiles[mine] = x;
+      if (mine >= 0) {
+        a.tiles[mine] = x;
+        atomicMax(&most, (int)takes);
+      }
       from = x.at;
       to = x.at + takes;
       cost += all;
@@ -103,7 +109,7 @@ __global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
     base = (int)min(base + total, (int64_t)a.cap);
     __syncthreads();
   }
-  const int64_t share = max((cost + a.S - 1) / a.S, (int64_t)MIN_SHARE);
+  const int64_t share = max((cost + a.S - 1) / a.S, (int64_t)max(MIN_SHARE, (int)sqrtf((float)most * a.balance)));
   if (tid == 0) *a.head = ChunkHead{share, base, 0};
   for (int s = tid; s < a.S; s += NT)
     if (s * share >= cost) a.start[s] = base;               // nothing to do
@@ -125,9 +131,14 @@ __global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
 // between slots s and s + 1, if it is the first of its tile, a head tile and the
 // CW columns of a wave.  Parts lie as in that wave's registers, 4 elements a lane:
 // run i of 64 lanes holds, of column n = lane % CW, elements e(i, lane) .. + 3.
-template <typename O, int D, int COLS, int CW>
-__global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
+// A wave takes a quarter of the runs.  Of PG sets of four waves each takes every
+// PG-th AT_ONCE parts, and the first adds up what the others have.
+template <typename O, int D, int COLS, int CW, int PG>
+__global__ __launch_bounds__(256 * PG) void join_kernel(ChunkArgs a) {
   constexpr int NR = CW * D / 256;                           // runs of a wave's columns
+  constexpr int OTHERS = PG > 1 ? PG - 1 : 1;
+  __shared__ f32x4 sums[OTHERS][PG > 1 ? 4 : 1][NR / 4][64];
+  __shared__ float2 stats[OTHERS][4][64];
   const int heads = a.Hkv * a.MT, waves = COLS / CW;
   const int wave = blockIdx.x % waves, hm = blockIdx.x / waves % heads, s = blockIdx.x / waves / heads;
   const int tile = a.start[s + 1];
@@ -137,9 +148,10 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
   if (t.at >= (s + 1) * share || t.at / share != s) return;  // begins at the cut, or has one in front
   const int last = (int)((to - 1) / share);
   const int h = hm / a.MT, mt = hm - h * a.MT, gt = min(a.GT, a.G - mt * a.GT);
-  const int lane = lane_id(), i0 = threadIdx.x >> 6;
+  const int lane = lane_id(), i0 = (threadIdx.x >> 6) & 3, set = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int col = wave * CW + lane % CW, my_row = col / a.GT, my_head = col - my_row * a.GT;
-  if (my_row >= t.rows || my_head >= gt) return;
+  const bool mine = my_row < t.rows && my_head < gt;
+  if (PG == 1 && !mine) return;
   auto part = [&](int i) { return ((size_t)(i == s ? 2 * s + 1 : 2 * i) * heads + hm) * COLS; };
   // A running reference, as the keys have: one pass, the next parts on their way.
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
@@ -148,8 +160,18 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
   f32x4 acc[NR / 4];
 #pragma unroll
   for (int k = 0; k < NR / 4; ++k) acc[k] = zero4();
+  auto add = [&](float c, float l, const f32x4 (&o)[NR / 4]) {
+    if (l == -1.f) return;                                   // saw nothing
+    any = true;
+    if (c == -INFINITY) { if (!(l <= 0.f)) sum += l; return; }     // scores of -inf alone, or NaN
+    const float top = fmaxf(m, c), w = __builtin_amdgcn_exp2f(c - top), f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
+    m = top;
+    sum = fmaf(l, w, sum * f);
+#pragma unroll
+    for (int k = 0; k < NR / 4; ++k) acc[k] = acc[k] * f + w * o[k];
+  };
   constexpr int AT_ONCE = NR > 16 ? 2 : 4;
-  for (int i = s; i <= last; i += AT_ONCE) {
+  for (int i = s + set * AT_ONCE; i <= last; i += PG * AT_ONCE) {
     float2 x[AT_ONCE];
     f32x4 o[AT_ONCE][NR / 4];
 #pragma unroll
@@ -161,18 +183,27 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
       for (int k = 0; k < NR / 4; ++k) o[j][k] = *reinterpret_cast<const f32x4*>(from + (i0 + 4 * k) * 256);
     }
 #pragma unroll
-    for (int j = 0; j < AT_ONCE; ++j) {
-      const float c = x[j].x, l = x[j].y;
-      if (i + j > last || l == -1.f) continue;               // saw nothing
-      any = true;
-      if (c == -INFINITY) { if (!(l <= 0.f)) sum += l; continue; }   // scores of -inf alone, or NaN
-      const float top = fmaxf(m, c), w = __builtin_amdgcn_exp2f(c - top), f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
-      m = top;
-      sum = fmaf(l, w, sum * f);
-#pragma unroll
-      for (int k = 0; k < NR / 4; ++k) acc[k] = acc[k] * f + w * o[j][k];
-    }
+    for (int j = 0; j < AT_ONCE; ++j)
+      if (i + j <= last) add(x[j].x, x[j].y, o[j]);
   }
+  if (PG > 1 && last - s >= AT_ONCE) {                                 // more than one set has parts
+    if (set > 0) {
+      stats[set - 1][i0][lane] = float2{m, any ? sum : -1.f};
+#pragma unroll
+      for (int k = 0; k < NR / 4; ++k) sums[set - 1][i0][k][lane] = acc[k];
+    }
+    __syncthreads();
+    if (set == 0)
+#pragma unroll
+      for (int j = 0; j < PG - 1; ++j) {
+        const float2 x = stats[j][i0][lane];
+        f32x4 o[NR / 4];
+#pragma unroll
+        for (int k = 0; k < NR / 4; ++k) o[k] = sums[j][i0][k][lane];
+        add(x.x, x.y, o);
+      }
+  }
+  if (set > 0 || !mine) return;
   const size_t rq = (size_t)(t.row0 + my_row) * a.Hq + h * a.G + mt * a.GT + my_head;
 #pragma unroll
   for (int k = 0; k < NR / 4; ++k) {
@@ -188,7 +219,7 @@ __global__ __launch_bounds__(256) void join_kernel(ChunkArgs a) {
 // LDS; 16 x 16 x 4 products, which bound it (the 3.6 GFLOP above would take 23 us
 // at the 154 TFLOP/s of a large product).  The next stage on its way through
 // registers while one is used: 117 us -> 80 for all three kernels, four workgroups
-// a CU instead of two: 71.
+// a CU instead of two: 71 to 73.
 constexpr int SK = 32, COLS32 = 64;
 
 template <typename O, int D>
@@ -362,15 +393,24 @@ template <typename O, int D> hipError_t launch32(const ChunkArgs& a, hipStream_t
   return hipGetLastError();
 }
 
+// Sets of waves only where tiles have many parts: elsewhere nearly all workgroups
+// have nothing to do, and larger ones take longer to say so.  (8 rows over 100000
+// tokens, 8 / 1 heads of 128, 112 parts: 57 us, 75 with one set; 8 prompts of up
+// to 2048 tokens, 16 / 16 heads of 64, up to 2: 98 us with four sets, 89 with one.)
+template <typename O, int D, int COLS, int CW> hipError_t launch_join(const ChunkArgs& a, hipStream_t s) {
+  constexpr int SETS = CW * D / 256 > 16 ? 2 : 4;            // what LDS holds
+  const int groups = (a.S - 1) * a.Hkv * a.MT * (COLS / CW);
+  if (a.S > 8 * (a.cap - 2)) hipLaunchKernelGGL((join_kernel<O, D, COLS, CW, SETS>), dim3(groups), dim3(256 * SETS), 0, s, a);
+  else hipLaunchKernelGGL((join_kernel<O, D, COLS, CW, 1>), dim3(groups), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 template <typename O, int D> hipError_t launch_d(const ChunkArgs& a, int dtype, int o_dtype, hipStream_t s) {
   if (a.B + 2 <= 256 && a.cap <= 256) hipLaunchKernelGGL(plan_kernel<256>, dim3(1), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(plan_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
   hipError_t e = dtype == 0 ? launch32<O, D>(a, s) : launch_chunk16(a, dtype, o_dtype, D, s);
   if (e != hipSuccess || a.S == 1) return e;
-  const int cuts = (a.S - 1) * a.Hkv * a.MT;
-  if (dtype == 0) hipLaunchKernelGGL((join_kernel<O, D, COLS32, 16>), dim3(cuts * (COLS32 / 16)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((join_kernel<O, D, CHUNK16_COLS, 32>), dim3(cuts * (CHUNK16_COLS / 32)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return dtype == 0 ? launch_join<O, D, COLS32, 16>(a, s) : launch_join<O, D, CHUNK16_COLS, 32>(a, s);
 }
 
 template <typename O> hipError_t launch_o(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {
@@ -384,8 +424,15 @@ template <typename O> hipError_t launch_o(const ChunkArgs& a, int dtype, int o_d
 int chunk_columns(int dtype) { return dtype == 0 ? COLS32 : CHUNK16_COLS; }
 
 // Two workgroups a CU, one where its LDS holds no more (16 bits, D = 256), four
-// where registers and LDS hold them (fp32, D = 64: 71 us for the prompts above, 80 with two).
+// where registers and LDS hold them (fp32, D = 64: 73 us for the prompts above, 80 with two).
 int chunk_groups(int dtype, int d) { return dtype == 0 ? (d == 64 ? 1024 : 512) : d == 256 ? 256 : 512; }
+
+// A tile of n blocks in shares of b is n / b parts for the join, which takes as
+// long as b blocks do where b^2 is about this much of n.  (1/8, 1/3, 1/2: 4 rows
+// over 30000 tokens, 32 / 8 heads of 128, bf16, 48, 45 and 40 us; 2 rows over 131072,
+// 16 / 2 of 256, 131, 121 and 124; 16 over 4096 23.7, 23.7 and 24.4; fp32, 4 rows over
+// 8000, 8 / 2 of 64, 32, 38 and 46.)
+float chunk_balance(int dtype) { return dtype == 0 ? 1.f / 8 : 1.f / 3; }
 
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {
   if (o_dtype == 1) return launch_o<bf16>(a, dtype, o_dtype, d, s);

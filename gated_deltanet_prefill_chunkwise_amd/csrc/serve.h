@@ -51,6 +51,7 @@ struct ChunkArgs {
   int TR, GT, MT;            // rows of a tile, query heads of one, head tiles of a group
   int cap;                   // tiles at most
   int S;                     // slots: workgroups of each head tile
+  float balance;             // a share's square, of the longest tile's blocks
   float scale;               // of the scores, times log2(e)
 };
 
@@ -62,6 +63,7 @@ hipError_t launch_rope(const RopeArgs& a, int dtype, int w_dtype, bool norm, boo
 // workgroups that fill the chip.
 int chunk_columns(int dtype);
 int chunk_groups(int dtype, int d);
+float chunk_balance(int dtype);
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s);
 
 }  // namespace sgdn

@@ -176,6 +176,7 @@ int sgdn_paged_attend_chunk(const sgdn_paged* p, const void* q, int64_t ldq, con
   a.R = p->rows; a.B = p->batch; a.Hq = p->n_q; a.Hkv = p->n_kv; a.G = p->n_q / p->n_kv;
   a.lp = log2_page(p->page); a.n_pages = p->n_pages; a.W = p->width; a.max_len = longest(p);
   a.TR = pl.TR; a.GT = pl.GT; a.MT = pl.MT; a.cap = pl.cap; a.S = pl.S;
+  a.balance = chunk_balance(p->dtype);
   a.scale = scale * 1.4426950408889634f;
   return launch_chunk(a, p->dtype, p->o_dtype, p->d, static_cast<hipStream_t>(stream)) == hipSuccess
              ? SGDN_OK : SGDN_EHIP;

@@ -288,3 +288,17 @@ def test_binding_refusals():
         assert e.value.status == status
     none, _ = call(q=q[:0])
     assert none.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("Hq, Hkv, D, P, dtype, new, cached", [
+    (8, 1, 128, 64, "bf16", 3, 60000), (4, 1, 64, 16, "f16", 1, 30000), (2, 1, 256, 32, "bf16", 2, 20011), (3, 1, 64, 16, "f32", 5, 12000),
+    (2, 1, 256, 64, "f32", 1, 9000), (4, 2, 128, 64, "f32", 2, 9000),
+])
+def test_few_rows_over_long_contexts(Hq, Hkv, D, P, dtype, new, cached):
+    """Tiles of many parts, which several sets of waves join; a context with a hole as long as some of them."""
+    cu, lens, rows = _step([(new, cached)], behind=1)
+    c = Case(cached, lens, Hq, Hkv, D, P, dtype)
+    c.table[0, 2000 // P:8000 // P] = -1
+    q = c.q(rows)
+    o, lse = _run(c, q, cu, lens)
+    check(o, lse, _want(c, q, cu, lens), "f32", dtype, D)
