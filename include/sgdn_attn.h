@@ -56,7 +56,8 @@
  *   no longer than the rows fill are therefore faster; so are a call of its
  *   own for a row that sees far more than the others, and for the prompts of a
  *   step that has single rows too.  Rows of one request read its context once
- *   each in sgdn_paged_attend.
+ *   each in sgdn_paged_attend; sgdn_paged_attend_chunk (sgdn_serve.h) reads it
+ *   once for many and divides its work by the lengths it finds.
  * - Alignment: q, k, v, the caches, codes and o start at 16 bytes; row
  *   strides are multiples of 16 bytes.  Otherwise SGDN_EINVAL.
  */
