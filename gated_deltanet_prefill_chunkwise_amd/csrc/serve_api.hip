@@ -74,7 +74,7 @@ int rope(const sgdn_rope_shape* p, const void* q, const void* k, bool norm, cons
 
 struct ChunkPlan { int cap, TR, GT, MT, S; size_t off_tiles, off_start, off_o, off_ml, total; };
 
-// False where a launch does not hold the heads.
+// False where the end of a block of keys would pass 32 bits.
 bool chunk_plan(const sgdn_paged* p, ChunkPlan* pl) {
   const int cols = chunk_columns(p->dtype), G = p->n_q / p->n_kv;
   pl->GT = G < cols ? G : cols;
@@ -84,7 +84,7 @@ bool chunk_plan(const sgdn_paged* p, ChunkPlan* pl) {
   // front and behind); rows < 2^26, so that 32 bits hold them
   const int64_t cap = ((int64_t)p->rows + pl->TR - 1) / pl->TR + (p->batch < p->rows ? p->batch : p->rows) + 2;
   const int64_t heads = (int64_t)p->n_kv * pl->MT, groups = chunk_groups(p->dtype, p->d);
-  if (too_many(heads, 256)) return false;
+  if (longest(p) > INT32_MAX - 127) return false;
   pl->cap = (int)cap;
   pl->S = (int)(groups > heads ? groups / heads : 1);
   const size_t parts = 2 * (size_t)pl->S * heads * cols;

@@ -152,8 +152,8 @@ size_t sgdn_paged_chunk_workspace_bytes(const sgdn_paged* p);
  * key).  A row's bits may depend on the other rows of its request and on the
  * lengths of the call's requests, by which the sums are divided; its error
  * bound does not.  Equal calls give equal bits.
- * n_kv ceil(n_q / n_kv / 128) < 2^24 - 7 (64 for 128 in fp32); SGDN_EUNSUPPORTED
- * otherwise. */
+ * A row sees at most 2^31 - 128 tokens: SGDN_EUNSUPPORTED where max_len, or width
+ * page without it, is larger. */
 int sgdn_paged_attend_chunk(const sgdn_paged* p, const void* q, int64_t ldq, const void* k_cache,
                             const void* v_cache, const int32_t* table, const int32_t* cu,
                             const int32_t* lens, float scale, void* o, float* lse, void* ws,

@@ -176,8 +176,9 @@ CHUNK_REFUSED = [
     (dict(rows=-1), EINVAL), (dict(n_q=0), EINVAL), (dict(n_kv=0), EINVAL), (dict(d=0), EINVAL), (dict(page=0), EINVAL),
     (dict(n_pages=0), EINVAL), (dict(dtype=3), EINVAL), (dict(o_dtype=3), EINVAL), (dict(d=96), EUNSUPPORTED),
     (dict(page=48), EUNSUPPORTED), (dict(n_q=9), EUNSUPPORTED), (dict(n_pages=1 << 26), EUNSUPPORTED),
-    (dict(rows=1 << 26), EUNSUPPORTED), (dict(n_q=(1 << 24) - 7, n_kv=(1 << 24) - 7), EUNSUPPORTED), (dict(batch=0), EINVAL), (dict(width=0), EINVAL), (dict(max_len=-1), EINVAL),
+    (dict(rows=1 << 26), EUNSUPPORTED), (dict(n_kv=65536, n_q=65536), EUNSUPPORTED), (dict(batch=0), EINVAL), (dict(width=0), EINVAL), (dict(max_len=-1), EINVAL),
     (dict(max_len=20 * 64 + 1), EINVAL), (dict(width=1 << 26), EUNSUPPORTED),
+    (dict(width=(1 << 25) - 1), EUNSUPPORTED), (dict(width=(1 << 25) - 1, max_len=(1 << 31) - 127), EUNSUPPORTED),
     (dict(scale=float("nan")), EINVAL), (dict(scale=3e38), EINVAL), (dict(ldq=1020), EINVAL), (dict(ldq=1028), EINVAL),
 ]
 
@@ -201,6 +202,9 @@ def test_chunk_pointers(L):
 def test_chunk_workspace(L):
     need = L.sgdn_paged_chunk_workspace_bytes(ctypes.byref(_shape()))
     assert need > 0
+    # the longest contexts, the most rows and heads: sizes beyond 32 bits are held
+    assert L.sgdn_paged_chunk_workspace_bytes(ctypes.byref(_shape(width=(1 << 25) - 1, max_len=(1 << 31) - 128))) > 0
+    assert L.sgdn_paged_chunk_workspace_bytes(ctypes.byref(_shape(rows=1 << 24, batch=1 << 30))) > 32 << 24
     assert _chunk(L, ws_bytes=need - 1) == EWORKSPACE
     assert _chunk(L, rows=0, ptr={n: None for n in ("q", "kc", "vc", "table", "cu", "lens", "o", "ws")}) == 0
 
