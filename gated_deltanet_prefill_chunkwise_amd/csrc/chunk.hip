@@ -56,7 +56,7 @@ __global__ __launch_bounds__(NT) void plan_kernel(ChunkArgs a) {
     for (int w = 0; w < NW; ++w) { if (w < wave) before += part[w]; total += part[w]; }
     return before;
   };
-  if (tid == 0) most = 0;              // blocks of the longest tile
+  if (tid == 0) most = 0;              // units of the longest tile
   int base = 0, mine = -1;             // this thread's tile of the last step
   int64_t cost = 0, from = 0, to = 0;  // ... and what it takes
   for (int64_t b0 = 0; b0 < (int64_t)a.B + 2; b0 += NT) {

@@ -51,7 +51,7 @@ struct ChunkArgs {
   int TR, GT, MT;            // rows of a tile, query heads of one, head tiles of a group
   int cap;                   // tiles at most
   int S;                     // slots: workgroups of each head tile
-  float balance;             // a share's square, of the longest tile's blocks
+  float balance;             // a share's square at least, of the longest tile's units
   float scale;               // of the scores, times log2(e)
 };
 
