@@ -12,11 +12,10 @@
 // So nothing crosses lanes between the products, and the running maximum, which
 // moves only where a score exceeds it by a threshold, is rarely shared.
 //
-// Weights enter the second product rounded to the type: for a 16-bit output in
-// one part, an error of half a step of the type like the output's own rounding;
-// for an fp32 output in two, the second what the rounding of the first left.
-// (A prompt of 8192 tokens below: 618 us in one part, 770 in two, for half as
-// many products again.)  All else is fp32.
+// Weights enter the second product in two parts, the number rounded to the type
+// and what that left, itself rounded, whatever the output's type: errors as in
+// paged_attend.hip.  In one part a 16-bit output errs by 1.4 times its own
+// rounding (2.3e-3 of a prompt in bf16, 1.7e-3 with two).  All else is fp32.
 //
 // Bound: the matrix cores' power.  32 / 8 heads of 128, bf16, page 64:
 //   a prompt of 8192 tokens    546 us, 1007 TFLOP/s (a library product of
@@ -42,7 +41,7 @@ namespace sgdn {
 namespace {
 
 constexpr int KB = CHUNK_KEYS, COLS = CHUNK16_COLS, NW = 4;
-constexpr int GROUP = 6;               // instructions behind a product (6, 8, 10: 785, 790, 793 us, two parts)
+constexpr int GROUP = 6;               // instructions behind a product (6, 8, 10: 785, 790, 793 us)
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -102,7 +101,7 @@ template <int D, bool V, int J = 0> __device__ __forceinline__ void copy_rows(co
   }
 }
 
-template <typename E, typename O, int D, int PARTS>
+template <typename E, typename O, int D>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(ChunkArgs a) {
   constexpr int NS = D / 16, DT = D / 32;            // reduction steps of the scores, 32-element tiles of an output
   constexpr int U = D / 8;                           // 16-byte units of a row
@@ -351,10 +350,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
           const float p0 = weight(i, r), p1 = weight(i, r + 1);
           l += p0 + p1;
           hi[r >> 1] = pack2<E>(p0, p1);
-          if (PARTS == 2) lo[r >> 1] = pack2<E>(rest_low<E>(p0, hi[r >> 1]), rest_high<E>(p1, hi[r >> 1]));
+          lo[r >> 1] = pack2<E>(rest_low<E>(p0, hi[r >> 1]), rest_high<E>(p1, hi[r >> 1]));
         }
         ph[i & 1] = __builtin_bit_cast(frag_t<E>, hi);
-        if (PARTS == 2) pl[i & 1] = __builtin_bit_cast(frag_t<E>, lo);
+        pl[i & 1] = __builtin_bit_cast(frag_t<E>, lo);
       };
       weights(0);
 #pragma unroll
@@ -366,14 +365,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int d = 0; d < DT; ++d) acc[d] = mma32(vf[i & 1][d], ph[i & 1], acc[d]);
-        if (PARTS == 2) {
 #pragma unroll
-          for (int d = 0; d < DT; ++d) acc[d] = mma32(vf[i & 1][d], pl[i & 1], acc[d]);
-        }
+        for (int d = 0; d < DT; ++d) acc[d] = mma32(vf[i & 1][d], pl[i & 1], acc[d]);
         if (i < 3) {
           weights(i + 1);
 #pragma unroll
-          for (int m = 0; m < DT * PARTS; ++m) {       // a product, then as many others as hide behind it
+          for (int m = 0; m < 2 * DT; ++m) {       // a product, then as many others as hide behind it
             __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x402, GROUP, 0);
           }
@@ -439,7 +436,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
 }
 
 template <typename E, typename O, int D> hipError_t launch_d(const ChunkArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((chunk16_kernel<E, O, D, __is_same(O, float) ? 2 : 1>), dim3((unsigned)(a.S * a.Hkv * a.MT)), dim3(64 * NW), 4 * KB * D * sizeof(E) + NW * 16 * 32 * sizeof(float), s, a);
+  hipLaunchKernelGGL((chunk16_kernel<E, O, D>), dim3((unsigned)(a.S * a.Hkv * a.MT)), dim3(64 * NW), 4 * KB * D * sizeof(E) + NW * 16 * 32 * sizeof(float), s, a);
   return hipGetLastError();
 }
 

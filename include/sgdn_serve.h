@@ -145,11 +145,8 @@ size_t sgdn_paged_chunk_workspace_bytes(const sgdn_paged* p);
  * nothing (rows of no request among them: o = 0, lse = -inf), pages that are
  * none, types, supported shapes.  Where cu falls, which request a row belongs
  * to is undefined, and rows may be left unwritten.
- * Precision: as sgdn_paged_attend, but with 16-bit inputs the softmax weights
- * enter their product rounded to the type where o is 16-bit too (an error of at
- * most 2^-8 in bf16, 2^-11 in fp16, of the weighted mean of |v|), and in two
- * parts where it is fp32 (2^-17; 2^-23 and 2^-35 of the largest weight for each
- * key).  A row's bits may depend on the other rows of its request and on the
+ * Precision: as sgdn_paged_attend, weights of 16-bit inputs in two parts
+ * whatever o's type.  A row's bits may depend on the other rows of its request and on the
  * lengths of the call's requests, by which the sums are divided; its error
  * bound does not.  Equal calls give equal bits.
  * A row sees at most 2^31 - 128 tokens: SGDN_EUNSUPPORTED where max_len, or width
