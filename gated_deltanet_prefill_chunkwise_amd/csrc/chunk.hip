@@ -163,7 +163,12 @@ __global__ __launch_bounds__(256 * PG) void join_kernel(ChunkArgs a) {
   auto add = [&](float c, float l, const f32x4 (&o)[NR / 4]) {
     if (l == -1.f) return;                                   // saw nothing
     any = true;
-    if (c == -INFINITY) { if (!(l <= 0.f)) sum += l; return; }     // scores of -inf alone, or NaN
+    if (c == -INFINITY) {                                    // scores of -inf alone, or NaN: sums of 0, or NaN
+      if (!(l <= 0.f)) sum += l;
+#pragma unroll
+      for (int k = 0; k < NR / 4; ++k) acc[k] += o[k];
+      return;
+    }
     const float top = fmaxf(m, c), w = __builtin_amdgcn_exp2f(c - top), f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
     m = top;
     sum = fmaf(l, w, sum * f);
