@@ -156,12 +156,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void chunk16_kernel(Chun
     // Here, once: a wait for them inside the loop would also wait for the copies there.
     __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0)
     // A negative scale turns the query's sign, so that the largest product is the largest score.
-    // A scale of 0 goes into the query whole, as 0 times a masked score is no score.
+    // A scale of 0 goes into the query whole, as 0 times a masked score is no score
+    // (and 0 times an element that is not finite is NaN, as the scaled score would be).
     if (a.scale <= 0.f) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qf[s][e] = a.scale == 0.f ? from_f<E>(0.f) : -qf[s][e];
+        for (int e = 0; e < 8; ++e) qf[s][e] = a.scale == 0.f ? from_f<E>(0.f * to_f(qf[s][e])) : -qf[s][e];
     }
     const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
     float c = -INFINITY, l = 0.f;
