@@ -20,6 +20,7 @@
 // reads the parts once, four at a time (one by one: 13.4 us for the 16 rows) and by
 // four sets of waves (one set: 9.2).
 #include "chunk.h"
+#include "chunk_rules.h"
 
 namespace sgdn {
 
@@ -398,20 +399,16 @@ template <typename O, int D> hipError_t launch32(const ChunkArgs& a, hipStream_t
   return hipGetLastError();
 }
 
-// Sets of waves only where tiles have many parts: elsewhere nearly all workgroups
-// have nothing to do, and larger ones take longer to say so.  (8 rows over 100000
-// tokens, 8 / 1 heads of 128, 112 parts: 57 us, 75 with one set; 8 prompts of up
-// to 2048 tokens, 16 / 16 heads of 64, up to 2: 98 us with four sets, 89 with one.)
 template <typename O, int D, int COLS, int CW> hipError_t launch_join(const ChunkArgs& a, hipStream_t s) {
   constexpr int SETS = CW * D / 256 > 16 ? 2 : 4;            // what LDS holds
   const int groups = (a.S - 1) * a.Hkv * a.MT * (COLS / CW);
-  if (a.S > 8 * (a.cap - 2)) hipLaunchKernelGGL((join_kernel<O, D, COLS, CW, SETS>), dim3(groups), dim3(256 * SETS), 0, s, a);
+  if (chunk_many_parts(a.S, a.cap)) hipLaunchKernelGGL((join_kernel<O, D, COLS, CW, SETS>), dim3(groups), dim3(256 * SETS), 0, s, a);
   else hipLaunchKernelGGL((join_kernel<O, D, COLS, CW, 1>), dim3(groups), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename O, int D> hipError_t launch_d(const ChunkArgs& a, int dtype, int o_dtype, hipStream_t s) {
-  if (a.B + 2 <= 256 && a.cap <= 256) hipLaunchKernelGGL(plan_kernel<256>, dim3(1), dim3(256), 0, s, a);
+  if (chunk_small(a.B, a.cap)) hipLaunchKernelGGL(plan_kernel<CHUNK_SMALL_PLAN>, dim3(1), dim3(CHUNK_SMALL_PLAN), 0, s, a);
   else hipLaunchKernelGGL(plan_kernel<1024>, dim3(1), dim3(1024), 0, s, a);
   hipError_t e = dtype == 0 ? launch32<O, D>(a, s) : launch_chunk16(a, dtype, o_dtype, D, s);
   if (e != hipSuccess || a.S == 1) return e;

@@ -81,7 +81,7 @@ bool chunk_plan(const sgdn_paged* p, ChunkPlan* pl) {
   pl->MT = (G + pl->GT - 1) / pl->GT;
   pl->TR = cols / pl->GT;
   // each request has one tile that is not full, and so have the rows of none (in
-  // front and behind); rows < 2^26, so that 32 bits hold them
+  // front and behind); rows < 2^28, so that there are under 2^29 + 2
   const int64_t cap = ((int64_t)p->rows + pl->TR - 1) / pl->TR + (p->batch < p->rows ? p->batch : p->rows) + 2;
   const int64_t heads = (int64_t)p->n_kv * pl->MT, groups = chunk_groups(p->dtype, p->d);
   if (longest(p) > INT32_MAX - 127) return false;
