@@ -1,11 +1,41 @@
-"""The attention of chunks where parts of a tile see nothing but scores of minus infinity, and at a scale
-of 0."""
+"""The attention of chunks where its plan takes many steps, where parts of a tile see nothing but
+scores of minus infinity, and at a scale of 0."""
+import numpy as np
 import pytest
 
+from oracle import paged as pref
+from oracle import serve as ref
 from test_gpu_chunk import _run, _step, _want, check
-from test_gpu_paged import Case, _i32
+from test_gpu_paged import Case, _f64, _i32
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_tiles_than_steps_of_the_plan_take(dtype):
+    """2500 tiles (128 heads a group: a row each) of three requests in one step of requests, two borders of
+    1024 tiles among them, rows of no request on both sides.  Rows at the borders against the oracle; all
+    of them against single rows, each side within 2^-10 (an error of a score of D 2^-24 times at most
+    2^4, weights of 2^-17, both twice in a mean of |v| < 2^3)."""
+    from gated_deltanet_prefill_chunkwise_amd import ops
+    step, most = [(1100, 0), (0, 9), (900, 7), (500, 100)], 20
+    cu, lens, rows = _step(step, front=3, behind=4)
+    c = Case(21, lens, 128, 1, 64, 16, dtype)
+    q = c.q(rows)
+    o, lse = _run(c, q, cu, lens, max_len=most)
+    req, sees = ref.chunk_rows(cu, lens, rows, most)
+    at = np.unique(np.concatenate([np.arange(x - 3, x + 4) for x in (3, 3 + 1024, 3 + 1100, 3 + 2000, 3 + 2048, 3 + 2500)]))
+    at = at[(at >= 0) & (at < rows)]
+    want = pref.attend(_f64(q)[at], _f64(c.k), _f64(c.v), c.table, sees[at], req=req[at], max_len=most)
+    v = _f64(c.v)
+    want[2]["vmax"] = np.full(want[1].shape, np.abs(v[np.isfinite(v)]).max())
+    check(o[at], lse[at], want, "f32", dtype, 64)
+    p, pl = ops.paged_attend(q, c.k, c.v, _i32(c.table), _i32(sees), row_req=_i32(req), max_len=most, want_lse=True)
+    assert float((o - p).abs().max()) <= 2.0 ** -9
+    none = (sees <= 0).nonzero()[0]
+    assert len(none) == 7 and not o[none].any() and bool((lse[none] == -float("inf")).all())
+    some = sees > 0
+    assert float((lse - pl)[some].abs().max()) <= 2.0 ** -9
 
 
 @pytest.mark.parametrize("dtype, D", [("bf16", 64), ("f16", 128), ("f32", 64)])
