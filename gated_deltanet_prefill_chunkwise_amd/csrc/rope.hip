@@ -23,7 +23,8 @@
 // Angles: t = p f in fp64 with the rounding error of the product carried
 // along, minus the nearest multiple n of pi/2 (as two fp64 numbers); what is
 // left, at most pi/4, goes to fp32 and into Taylor polynomials (the first
-// dropped terms are under 2e-9), and n mod 4 says which is which.
+// dropped terms are under 2e-9), and n mod 4 says which is which.  (Positions
+// give angles far below 2^50, up to where n is the nearest but for a quarter.)
 //
 // Norm: squares are summed in fp64, so that heads of any magnitude are normed
 // alike (fp32 sums: 188 us of 193); where 1 / norm may lie outside fp32, x is
@@ -44,10 +45,11 @@ __device__ __forceinline__ float2 turn(double p, double f) {
   const double n = rint(t * 0.63661977236758134308);                  // 2 / pi
   double r = fma(-n, 1.57079632679489655800e+00, t);                  // pi / 2: the nearest fp64 number
   r = fma(-n, 6.12323399573676603587e-17, r) + low;                   // and what it leaves
+  if (fabs(r) > 2.0) r = 0.0;              // t past 2^52: n is off by more than the angle is known to, any turn will do
   const float x = (float)r, y = x * x;
   const float s = x * (1.f + y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880)))));
   const float c = 1.f + y * (-0.5f + y * (1.f / 24 + y * (-1.f / 720 + y * (1.f / 40320 + y * (-1.f / 3628800)))));
-  const int q = (int)(long long)n & 3;
+  const int q = (int)(n - 4.0 * floor(0.25 * n)) & 3;                 // 64 bits may not hold n
   return float2{q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s, q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c};
 }
 

@@ -101,7 +101,8 @@ typedef struct {
  *   freqs        [rot / 2] fp64, radians per token (sgdn_rope_freqs, or any)
  *   magnitude    finite
  * Angles are formed and reduced in fp64, exact to 2^-53 of themselves: a
- * position of 10^6 errs by 10^-10.  Values are turned in fp32 and rounded
+ * position of 10^6 errs by 10^-10.  (Beyond 2^52 nothing of an angle is known
+ * modulo a turn: pairs are turned by some angle.)  Values are turned in fp32 and rounded
  * once.  Elements behind rot are copied.
  * Alignment: q, k and their outputs start at 16 bytes, strides are multiples of
  * 16 bytes, freqs starts at 8; SGDN_EINVAL otherwise. */
