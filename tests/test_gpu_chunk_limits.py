@@ -1,10 +1,12 @@
 """The attention of chunks where its plan takes many steps, where parts of a tile see nothing but
-scores of minus infinity, and at a scale of 0."""
+scores of minus infinity, at a scale of 0, where wide fp32 heads hold values that are not finite, and
+where requests share pages."""
 import numpy as np
 import pytest
 
 from oracle import paged as pref
 from oracle import serve as ref
+import test_gpu_chunk as chunk
 from test_gpu_chunk import _run, _step, _want, check
 from test_gpu_paged import Case, _f64, _i32
 
@@ -73,3 +75,21 @@ def test_queries_that_are_not_finite_at_a_scale_of_zero(dtype, value):
     assert torch.isnan(o[7, 1]).all() and bool(torch.isnan(lse[7, 1]))
     o[7, 1], lse[7, 1] = clean[7, 1], clean_lse[7, 1]
     assert torch.equal(o, clean) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_later_tokens_do_not_reach_earlier_rows_of_wide_heads(D):
+    chunk.test_later_tokens_do_not_reach_earlier_rows("f32", D)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_requests_that_share_pages(dtype):
+    """A common beginning: the same pages in the tables of several requests, and twice in one."""
+    cu, lens, rows = _step([(40, 200), (3, 237), (1, 100), (70, 170)])
+    c = Case(24, lens, 8, 2, 64, 16, dtype)
+    c.table[1, :10] = c.table[0, :10]
+    c.table[2, :6] = c.table[0, 3]
+    c.table[3, 1:5] = c.table[0, 1:5]
+    q = c.q(rows)
+    o, lse = _run(c, q, cu, lens)
+    check(o, lse, _want(c, q, cu, lens), "f32", dtype, 64)
