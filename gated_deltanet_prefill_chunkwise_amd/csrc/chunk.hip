@@ -15,8 +15,8 @@
 // that where the longest tile would fall into more parts than are worth joining.
 //
 // Measured (plan, attention, join): 16 rows over 4096 tokens, 32 / 8 heads of 128,
-// bf16: 5.2, 11 and 7 us; fp32, 3 prompts of up to 301 rows over up to 1501 tokens,
-// 15 / 3 heads of 64: 6, 65 and 7 us.  The plan is latency (a chain of sums), the join
+// bf16: 5.1, 13.2 and 7.6 us; fp32, 3 prompts of up to 301 rows over up to 1501 tokens,
+// 15 / 3 heads of 64: 6.4, 64 and 7.2 us.  The plan is latency (a chain of sums), the join
 // reads the parts once, four at a time (one by one: 13.4 us for the 16 rows) and by
 // four sets of waves (one set: 9.2).
 #include "chunk.h"
@@ -222,10 +222,13 @@ __global__ __launch_bounds__(256 * PG) void join_kernel(ChunkArgs a) {
 }
 
 // fp32: 64 columns a tile, 16 a wave; keys and values in stages of 32 through
-// LDS; 16 x 16 x 4 products, which bound it (the 3.6 GFLOP above would take 23 us
-// at the 154 TFLOP/s of a large product).  The next stage on its way through
-// registers while one is used: 117 us -> 80 for all three kernels, four workgroups
-// a CU instead of two: 71 to 73.
+// LDS; 16 x 16 x 4 products (the 3.6 GFLOP above would take 23 us at the 154 TFLOP/s
+// of a large product).  The next stage on its way through registers while one is
+// used: 117 us -> 80 for all three kernels, four workgroups a CU instead of two: 71 to
+// 73.  A prompt of 4096, 32 / 8 heads of 128: 1490 us, products alone 893; 16 / 2 of
+// 256: 2600 us, as its accumulators lie in scratch (272 bytes a lane) and every stage
+// loads and stores them: the loops over values that are not finite are too large to
+// unroll there, so that they index the accumulators at run time.
 constexpr int SK = 32, COLS32 = 64;
 
 template <typename O, int D>
@@ -432,8 +435,9 @@ int chunk_groups(int dtype, int d) { return dtype == 0 ? (d == 64 ? 1024 : 512) 
 // A tile of n blocks in shares of b is n / b parts for the join, which takes as
 // long as b blocks do where b^2 is about this much of n.  (1/8, 1/3, 1/2: 4 rows
 // over 30000 tokens, 32 / 8 heads of 128, bf16, 48, 45 and 40 us; 2 rows over 131072,
-// 16 / 2 of 256, 131, 121 and 124; 16 over 4096 23.7, 23.7 and 24.4; fp32, 4 rows over
-// 8000, 8 / 2 of 64, 32, 38 and 46.)
+// 16 / 2 of 256, 131, 121 and 124; 16 over 4096 23.7, 23.7 and 24.4 (these with weights
+// in one part, a tenth faster or less); fp32, 4 rows over 8000, 8 / 2 of 64, 32, 38 and
+// 46.)
 float chunk_balance(int dtype) { return dtype == 0 ? 1.f / 8 : 1.f / 3; }
 
 hipError_t launch_chunk(const ChunkArgs& a, int dtype, int o_dtype, int d, hipStream_t s) {

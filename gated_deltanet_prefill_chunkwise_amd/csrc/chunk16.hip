@@ -17,21 +17,31 @@
 // paged_attend.hip.  In one part a 16-bit output errs by 1.4 times its own
 // rounding (2.3e-3 of a prompt in bf16, 1.7e-3 with two).  All else is fp32.
 //
-// Bound: the matrix cores' power.  32 / 8 heads of 128, bf16, page 64:
-//   a prompt of 8192 tokens    546 us, 1007 TFLOP/s (a library product of
-//                              8192^3: 1273); the clock falls to 1.9 GHz
+// Measured, 32 / 8 heads of 128, bf16, page 64:
+//   a prompt of 8192 tokens    720 to 775 us, 763 TFLOP/s (a library product of
+//                              8192^3: 1240 to 1273; half as many products
+//                              again are the weights' second parts)
 //   4 x up to 1024 tokens over 16384 cached and 60 single rows over as many
-//                              1080 us; 2.7 GB and 694 GFLOP would each take 545
-//   127 single rows over up to 8192 tokens   510 us, what reading the cache takes
-// and 16 / 2 heads of 256, 512 tokens over 131072: 1262 us, 871 TFLOP/s.
-// Of 3290 clocks a block 129 are waits for the copies; no LDS bank conflicts.
-// Tried (the prompt; boxes differ by 7 %): 8 waves and 256 columns 578 us against
-// 569, though the step of prompts and rows then reads 4.4 GB of HBM and not 7.3;
-// those 8 in halves half a block apart 1057 against 906 (prompts and rows); the
-// scores of the next 64 keys between the weights of these 710 against 618, of the
-// next 32 790 against 624 (registers).  A raised priority of waves that form
-// weights: 589 -> 581 us, prompts and rows 1150 -> 1115.  Waves that divide the
-// keys of single rows among them: 526 against 510 us (127 rows).
+//                              1304 to 1417 us; 2.7 GB and 694 GFLOP would each take 545
+//   127 single rows over up to 8192 tokens   409 us, what reading the cache takes
+// and 16 / 2 heads of 256, 512 tokens over 131072: 1571 to 1702 us, 700 TFLOP/s.
+// Bound: the prompt by both pipes together.  Of the cycles the matrix units are
+// busy 62 %, vector instructions issue in 55 %, any instruction in 74 %; waves wait
+// 17 % of their time; the clock falls from 2.2 to 1.6 GHz as calls follow each
+// other.  The fast loop is 48 products, 33 exponentials and some 430 others a
+// block, without spills (D = 128; 24 registers of the rare case lie in scratch);
+// no LDS bank conflicts.  Heads of 256: one wave a SIMD, matrix 50 %, vector 31 %,
+// any 44 %: what a wave does follows on itself.  Prompts and single rows: 49, 42
+// and 60 %, waits 33 %, and 7.4 GB read past the L2 (5.7 TB/s), where 2.7 would do;
+// which of the two holds it is not settled.  Heads of 64: 31, 51 and 68 %.
+// Tried, with weights in one part (the prompt; boxes differ by 7 %): 8 waves and
+// 256 columns 578 us against 569, though the step of prompts and rows then reads
+// 4.4 GB of HBM and not 7.3; those 8 in halves half a block apart 1057 against 906
+// (prompts and rows); the scores of the next 64 keys between the weights of these
+// 710 against 618, of the next 32 790 against 624 (registers).  A raised priority
+// of waves that form weights: 589 -> 581 us, prompts and rows 1150 -> 1115.  Waves
+// that divide the keys of single rows among them: 526 against 510 us (127 rows of
+// other lengths).
 #include <type_traits>
 
 #include "chunk.h"

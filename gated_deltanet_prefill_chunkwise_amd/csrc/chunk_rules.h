@@ -14,9 +14,12 @@ inline bool chunk_small(int B, int cap) { return (int64_t)B + 2 <= CHUNK_SMALL_P
 
 // Sets of waves in the join only where tiles have many parts: elsewhere nearly
 // all workgroups have nothing to do, and larger ones take longer to say so.  (8
-// rows over 100000 tokens, 8 / 1 heads of 128, 112 parts: 57 us, 75 with one set;
+// rows over 100000 tokens, 8 / 1 heads of 128, 112 parts: 61 us, 70 with one set;
 // 8 prompts of up to 2048 tokens, 16 / 16 heads of 64, up to 2: 98 us with four
-// sets, 89 with one.)
+// sets, 89 with one, weights then in one part.)  cap bounds the tiles from the
+// sizes alone: a step of fixed size whose table has 64 requests, one of them live,
+// takes the one set (those 8 rows with 120 behind them 70 us, 61 in a table of
+// one request).
 inline bool chunk_many_parts(int S, int cap) { return S > 8 * ((int64_t)cap - 2); }
 
 }  // namespace sgdn

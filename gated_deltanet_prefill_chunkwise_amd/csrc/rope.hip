@@ -18,6 +18,8 @@
 // 958 MB normed and turned in 193 us (5.0 TB/s; a copy reaches 4.99).  The
 // weights come by way of LDS, once a workgroup: read by each row from memory,
 // 2 bytes a load, they cost 237 us, and 316 us for those of both elements.
+// Halves by way of LDS (38932 rows, 60 of 128 turned): turned 155 us like the
+// others, normed and turned 227, where pairs in a lane take 170.
 // Waves that walk several rows, 8192 at a time: 166 and 226 us.
 //
 // Angles: t = p f in fp64 with the rounding error of the product carried
